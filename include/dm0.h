@@ -392,6 +392,98 @@ dm0_status dm0_set_prefix_fp8(dm0_ctx* ctx, int enable, void* stream);
  * pointers or a non-finite input, DM0_ESHAPE unless rows, cols >= 1. */
 dm0_status dm0_pack_e4m3_rows(const float* x, int64_t rows, int64_t cols, uint8_t* codes, float* scales);
 
+/* Language side of the VLM: token rows, the norms around a block, the vocabulary loss.
+ *
+ * The pages give these no equations of their own; they are the operators that stand before the prefix pass
+ * (token ids -> prefix rows), between the blocks of a time-modulated or twice-normed layer (DM0.5 page,
+ * section 5.2: a norm's scale and shift, a gate on the residual) and behind the last layer (the VLM's next-token
+ * loss, which knowledge insulation keeps training; DM0 architecture notes, section 1).
+ * Sizes come with each call and need not be the context's; eps is its rms_eps.  Scratch is the caller's
+ * `workspace` (16-byte aligned, at least the bytes the _workspace function names, which is 0 for sizes the
+ * call refuses): calls that may overlap on the GPU, or captured graphs that may, take different workspaces.
+ * Results do not depend on the order in which thread blocks run.  Every call allocates nothing, may be captured, and
+ * is asynchronous on `stream`; the current device must be the context's (DM0_EINVAL).  Device pointers of
+ * rows, gains and weights are 16-byte aligned (DM0_EINVAL).  batch * tokens is 1..2^24, vocab 1..2^22
+ * (DM0_ESHAPE).  Ids and targets are int32, or int64 where the _i64 argument is nonzero; a negative one means no
+ * token; one >= vocab counts as none and sets the device error word's bad-index bit. */
+
+/* out[b][t][:] = scale * table[ids[b][t]][:] in fp32, rounded once to out's type; a zero row for id < 0.
+ *   table: device bf16 [vocab][hidden]; ids: device [B][T];
+ *   out:   device fp32 (out_f32 != 0) or bf16; row (b, t) starts at element b * batch_stride + t * row_stride,
+ *          so text rows can be written behind a sample's image rows.  Strides are multiples of 16 bytes,
+ *          row_stride >= hidden.  hidden: a multiple of 8, at most 65536. */
+dm0_status dm0_embed(dm0_ctx* ctx, const void* table, const void* ids, int ids_i64, int B, int T, int vocab, int hidden,
+                     float scale, void* out, int out_f32, int64_t batch_stride, int64_t row_stride, void* stream);
+
+/* grad[v][:] = scale * sum of dout[b][t][:] over the positions with ids[b][t] = v, added in fp32 in an order that
+ * the ids fix; accumulate != 0 adds it to grad (rows without a token stay untouched), else every row is written.
+ *   dout: device fp32 or bf16, strided as dm0_embed's out; grad: device f32 [vocab][hidden]. */
+dm0_status dm0_embed_grad(dm0_ctx* ctx, const void* ids, int ids_i64, int B, int T, int vocab, int hidden, float scale,
+                          const void* dout, int dout_f32, int64_t batch_stride, int64_t row_stride, float* grad,
+                          int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+size_t dm0_embed_grad_workspace(int B, int T, int vocab, int hidden);
+
+/* Sizes, types and vectors of dm0_residual_norm.  Vectors are device f32 and may be null (a factor of one, a shift of
+ * zero).  gate, mod_scale and mod_shift hold a row of `hidden` values per sample, the rows gate_stride and
+ * mod_stride floats apart (multiples of 4), or one row for every sample (stride 0). */
+typedef struct {
+  int batch, tokens, hidden;   /* hidden: a multiple of 8, at most 8192 */
+  int h_f32, y_f32;            /* residual stream and block output: fp32 (nonzero) or bf16 */
+  float scale;                 /* of the residual */
+  const float* post_gain;      /* [hidden]: norm of the block output; null: no norm there */
+  const float* gate;
+  int gate_stride;
+  const float* pre_gain;       /* [hidden]: norm before the next block */
+  const float *mod_scale, *mod_shift;
+  int mod_stride;
+} dm0_norm;
+
+/* The boundary behind a block with output y on the residual stream h, per row and in fp32:
+ *   u = y r_post post_gain, r_post = 1 / sqrt(mean(y^2) + eps)   (u = y without post_gain)
+ *   h_out = scale h + gate u
+ *   n_out = h_out r_pre pre_gain (1 + mod_scale) + mod_shift, r_pre = 1 / sqrt(mean(h_out^2) + eps)
+ * with h_out not yet rounded to its type in the second norm.
+ *   h, h_out: device [batch][tokens][hidden] (may be the same); y: of its type, or null (h_out = scale h);
+ *   n_out: device bf16; r_post (null without post_gain), r_pre: device f32 [batch][tokens], for the gradient. */
+dm0_status dm0_residual_norm(dm0_ctx* ctx, const dm0_norm* args, const void* h, const void* y, void* h_out, void* n_out,
+                             float* r_post, float* r_pre, void* stream);
+
+/* Gradients of the vectors, device f32: [hidden], or dense [batch][hidden] where the vector is per sample; null: not
+ * wanted. */
+typedef struct {
+  float *post_gain, *gate, *pre_gain, *mod_scale, *mod_shift;
+} dm0_norm_grads;
+
+/* Adjoint of dm0_residual_norm from its h_out, y, r_post and r_pre:
+ *   dn: device fp32 or bf16, gradient of n_out; dh_out: gradient of h_out from the rest of the model, h's type, or null;
+ *   dh, dy: gradients of h and y, of their types (dh may be dh_out, dy may be y; null dy without y). */
+dm0_status dm0_residual_norm_grad(dm0_ctx* ctx, const dm0_norm* args, const void* dn, int dn_f32, const void* dh_out,
+                                  const void* h_out, const void* y, const float* r_post, const float* r_pre, void* dh,
+                                  void* dy, const dm0_norm_grads* grads, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+size_t dm0_residual_norm_grad_workspace(const dm0_norm* args);
+
+/* Softmax cross entropy over a vocabulary without keeping the logits z = hidden_states weight^T:
+ *   lse[i] = log sum_v exp(z[i][v]); loss[i] = lse[i] - z[i][targets[i]], 0 without a target.
+ *   hidden_states: device bf16 [tokens][hidden]; weight: device bf16 [vocab][hidden]; loss, lse: device f32 [tokens].
+ * hidden: a multiple of 64, at most 65536.  Products of bf16 values are added in fp32. */
+dm0_status dm0_vocab_loss(dm0_ctx* ctx, const void* hidden_states, const void* weight, const void* targets,
+                          int targets_i64, int tokens, int vocab, int hidden, float* loss, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+size_t dm0_vocab_loss_workspace(int tokens, int vocab, int hidden);
+
+/* Gradient of sum_i dloss[i] loss[i] from the lse of dm0_vocab_loss (dloss: device f32 [tokens], not read into the
+ * result where there is no target).  With G = (softmax - onehot) dloss, divided by the largest |dloss| and rounded to
+ * bf16 as the products' operand:
+ *   dhidden = G weight:          device fp32 or bf16 [tokens][hidden], or null
+ *   dweight = G^T hidden_states: device fp32 or bf16 [vocab][hidden], or null; accumulate != 0 (fp32 only) adds to it
+ * The logits are built again, in pieces of the vocabulary of at most 2^27 entries (256 MB of the workspace). */
+dm0_status dm0_vocab_loss_grad(dm0_ctx* ctx, const void* hidden_states, const void* weight, const void* targets,
+                               int targets_i64, const float* lse, const float* dloss, int tokens, int vocab, int hidden,
+                               void* dhidden, int dhidden_f32, void* dweight, int dweight_f32, int accumulate,
+                               void* workspace, size_t workspace_bytes, void* stream);
+size_t dm0_vocab_loss_grad_workspace(int tokens, int vocab, int hidden);
+
 /* Instrumentation. ------------------------------------------------------- */
 
 /* Number of kernels this context has enqueued so far (a replayed graph counts

@@ -16,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdm0.so")
 
 c_int, c_float, c_size_t, c_void_p = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+c_int64 = ctypes.c_int64
 
 STATUS = {0: "DM0_OK", -1: "DM0_EINVAL", -2: "DM0_ESHAPE", -3: "DM0_ENOMEM", -4: "DM0_ECUDA",
           -5: "DM0_EDEVICE", -6: "DM0_ESTATE"}
@@ -26,7 +27,10 @@ EXPORTS = ("dm0_create", "dm0_weights_bytes", "dm0_load_weights", "dm0_prefill",
            "dm0_op_attention", "dm0_attention_noalloc", "dm0_debug_view", "dm0_launch_count", "dm0_probe",
            "dm0_probe_read", "dm0_selftest_timeout", "dm0_sync", "dm0_device_error", "dm0_clear_error", "dm0_last_error",
            "dm0_destroy", "dm0_pack_e4m3_rows", "dm0_set_prefix_fp8", "dm0_op_quant_e4m3",
-           "dm0_op_gemm_e4m3", "dm0_grad_floats", "dm0_train_step", "dm0_prepare")
+           "dm0_op_gemm_e4m3", "dm0_grad_floats", "dm0_train_step", "dm0_prepare", "dm0_embed", "dm0_embed_grad",
+           "dm0_embed_grad_workspace", "dm0_residual_norm", "dm0_residual_norm_grad",
+           "dm0_residual_norm_grad_workspace", "dm0_vocab_loss", "dm0_vocab_loss_workspace", "dm0_vocab_loss_grad",
+           "dm0_vocab_loss_grad_workspace")
 
 
 class Dm0Config(ctypes.Structure):
@@ -34,6 +38,16 @@ class Dm0Config(ctypes.Structure):
                 ("inter_a", c_int), ("n_q", c_int), ("n_kv", c_int), ("head_dim", c_int),
                 ("chunk", c_int), ("action_dim", c_int), ("max_batch", c_int), ("max_prefix", c_int),
                 ("rope_theta", c_float), ("rms_eps", c_float), ("time_mod", c_int)]
+
+
+class Dm0Norm(ctypes.Structure):
+    _fields_ = [("batch", c_int), ("tokens", c_int), ("hidden", c_int), ("h_f32", c_int), ("y_f32", c_int),
+                ("scale", c_float), ("post_gain", c_void_p), ("gate", c_void_p), ("gate_stride", c_int),
+                ("pre_gain", c_void_p), ("mod_scale", c_void_p), ("mod_shift", c_void_p), ("mod_stride", c_int)]
+
+
+class Dm0NormGrads(ctypes.Structure):
+    _fields_ = [(k, c_void_p) for k in ("post_gain", "gate", "pre_gain", "mod_scale", "mod_shift")]
 
 
 class Dm0Error(RuntimeError):
@@ -85,6 +99,19 @@ def load_library() -> ctypes.CDLL:
         "dm0_grad_floats": (c_size_t, [P]),
         "dm0_prepare": (c_int, [P, c_int, c_int, c_int]),
         "dm0_train_step": (c_int, [P, P, P, P, P, P, P, P, P]),
+        "dm0_embed": (c_int, [P, P, P, c_int, c_int, c_int, c_int, c_int, c_float, P, c_int, c_int64, c_int64, P]),
+        "dm0_embed_grad": (c_int, [P, P, c_int, c_int, c_int, c_int, c_int, c_float, P, c_int, c_int64, c_int64, P,
+                                   c_int, P, c_size_t, P]),
+        "dm0_embed_grad_workspace": (c_size_t, [c_int, c_int, c_int, c_int]),
+        "dm0_residual_norm": (c_int, [P, ctypes.POINTER(Dm0Norm), P, P, P, P, P, P, P]),
+        "dm0_residual_norm_grad": (c_int, [P, ctypes.POINTER(Dm0Norm), P, c_int, P, P, P, P, P, P, P,
+                                           ctypes.POINTER(Dm0NormGrads), P, c_size_t, P]),
+        "dm0_residual_norm_grad_workspace": (c_size_t, [ctypes.POINTER(Dm0Norm)]),
+        "dm0_vocab_loss": (c_int, [P, P, P, P, c_int, c_int, c_int, c_int, P, P, P, c_size_t, P]),
+        "dm0_vocab_loss_workspace": (c_size_t, [c_int, c_int, c_int]),
+        "dm0_vocab_loss_grad": (c_int, [P, P, P, P, c_int, P, P, c_int, c_int, c_int, P, c_int, P, c_int, c_int, P,
+                                        c_size_t, P]),
+        "dm0_vocab_loss_grad_workspace": (c_size_t, [c_int, c_int, c_int]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -42,7 +42,9 @@
 #include "elementwise.cuh"
 #include "gemm.cuh"
 #include "ptx.cuh"
+#include "residual_norm.cuh"
 #include "train.cuh"
+#include "vocab_loss.cuh"
 
 using dm0::AttnArgs;
 using dm0::GemmArgs;
@@ -1250,6 +1252,7 @@ dm0_status pack_fp8_weights(dm0_ctx* c, cudaStream_t s) {
 }  // namespace
 
 #include "train_host.cuh"
+#include "language_host.cuh"
 
 extern "C" {
 
@@ -1415,7 +1418,7 @@ dm0_status dm0_create(const dm0_config* cfg, dm0_ctx** out) {
   auto smem_attr = [&](auto kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  bool ok = smem_attr(dm0::gemm_tc_kernel<64, kGemmStages>, dm0::GemmSmem<64, kGemmStages>::kBytes) &&
+  bool ok = lang_setup() && smem_attr(dm0::gemm_tc_kernel<64, kGemmStages>, dm0::GemmSmem<64, kGemmStages>::kBytes) &&
             smem_attr(dm0::gemm_tc_kernel<128, kGemmStages>, dm0::GemmSmem<128, kGemmStages>::kBytes) &&
             smem_attr(dm0::gemm_tc_kernel<256, kGemmStages>, dm0::GemmSmem<256, kGemmStages>::kBytes) &&
             smem_attr(dm0::gemm_tc_persistent<64, 8>, dm0::PGemmSmem<64, 8>::kBytes) &&

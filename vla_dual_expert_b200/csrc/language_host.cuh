@@ -1,0 +1,514 @@
+// Host side of the language operators (dm0_embed, dm0_residual_norm, dm0_vocab_loss and their gradients):
+// argument checks, workspace layouts, TMA maps and launches.  Included by dm0.cu after its dispatch
+// helpers (launch, fail, ...), whose definitions it uses.  All scratch is the caller's workspace, so calls on
+// different streams and captured graphs share nothing inside the context.
+#pragma once
+
+namespace {
+
+constexpr int kLangMaxTokens = 1 << 24, kLangMaxVocab = 1 << 22, kLangMaxHidden = 1 << 16;
+constexpr int kLangSms = 148;   // plans depend on sizes alone, so a workspace size holds for every context
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// The context part of every entry's checks: its device must be the current one.
+dm0_status lang_enter(dm0_ctx* c) {
+  if (!c) return DM0_EINVAL;
+  int dev = -1;
+  CK(cudaGetDevice(&dev));
+  if (dev != c->device)
+    return fail(c, DM0_EINVAL, "the context belongs to device " + std::to_string(c->device) + ", the current one is " +
+                                   std::to_string(dev));
+  c->pdl_ok = false;   // the first kernel follows foreign work
+  return DM0_OK;
+}
+
+bool lang_tokens_ok(int B, int T) {
+  return B >= 1 && T >= 1 && static_cast<int64_t>(B) * T <= kLangMaxTokens;
+}
+
+// ---------------------------------------------------------------- embedding
+dm0_status rows_ok(dm0_ctx* c, const void* p, int f32, int T, int H, int64_t batch, int64_t row) {
+  const int vec = f32 ? 4 : 8;
+  if (row < H || batch < 0 || row % vec != 0 || batch % vec != 0 || !aligned16(p))
+    return fail(c, DM0_EINVAL, "rows must be 16-byte aligned, their strides multiples of 16 bytes, row stride >= hidden");
+  return DM0_OK;
+}
+
+struct EmbGradPlan {
+  int rows, sort_ctas, tiles, slices, zero_ctas;
+  size_t perm, row_of, start, part, bytes;
+};
+EmbGradPlan emb_grad_plan(int n, int vocab, int H) {
+  EmbGradPlan p{};
+  p.rows = std::min(dm0::kSortMaxRows, std::max(1, (vocab + kLangSms - 1) / kLangSms));
+  p.sort_ctas = (vocab + p.rows - 1) / p.rows;
+  p.tiles = (n + dm0::kEmbTile - 1) / dm0::kEmbTile;
+  p.slices = (H + dm0::kEmbCols - 1) / dm0::kEmbCols;
+  p.zero_ctas = (vocab + dm0::kEmbZeroRows - 1) / dm0::kEmbZeroRows;
+  p.perm = 0;
+  p.row_of = align256(sizeof(int) * static_cast<size_t>(n));
+  p.start = 2 * p.row_of;
+  p.part = p.start + align256(sizeof(int) * (static_cast<size_t>(vocab) + 1));
+  p.bytes = p.part + align256(sizeof(float) * 2 * p.tiles * static_cast<size_t>(H));
+  return p;
+}
+
+template <typename Td>
+dm0_status embed_grad_run(dm0_ctx* c, cudaStream_t s, dm0::Ids ids, int n, const dm0::RowsView& v, int vocab, int H,
+                          float scale, const Td* dout, float* grad, int accumulate, uint8_t* ws) {
+  const EmbGradPlan p = emb_grad_plan(n, vocab, H);
+  int* perm = reinterpret_cast<int*>(ws + p.perm);
+  int* row_of = reinterpret_cast<int*>(ws + p.row_of);
+  int* start = reinterpret_cast<int*>(ws + p.start);
+  float* part = reinterpret_cast<float*>(ws + p.part);
+  TRY(launch(c, s, dm0::embed_sort_kernel, dim3(p.sort_ctas), dim3(dm0::kSortWarps * 32),
+             sizeof(int) * dm0::kSortWarps * p.rows, ids, n, vocab, p.rows, perm, row_of, start, c->d_err));
+  TRY(launch(c, s, dm0::embed_sum_kernel<Td>, dim3(p.tiles * p.slices + (accumulate ? 0 : p.zero_ctas)), dim3(256), 0,
+             static_cast<const int*>(perm), static_cast<const int*>(row_of), static_cast<const int*>(start), dout, v, n,
+             vocab, H, scale, grad, accumulate, part, p.tiles, p.slices));
+  if (p.tiles < 2) return DM0_OK;
+  return launch(c, s, dm0::embed_join_kernel, dim3(p.tiles - 1, (H + dm0::kFixCols - 1) / dm0::kFixCols), dim3(256), 0,
+                static_cast<const int*>(row_of), static_cast<const int*>(start), vocab, H, scale, grad, accumulate,
+                static_cast<const float*>(part));
+}
+
+// ---------------------------------------------------------------- residual norms
+dm0_status norm_ok(dm0_ctx* c, const dm0_norm* a) {
+  if (!a) return fail(c, DM0_EINVAL, "null argument");
+  if (!lang_tokens_ok(a->batch, a->tokens)) return fail(c, DM0_ESHAPE, "bad batch or tokens");
+  if (a->hidden < 8 || a->hidden % 8 != 0 || a->hidden > dm0::kRnMaxHidden)
+    return fail(c, DM0_ESHAPE, "the norms take hidden sizes of 8..8192, multiples of 8");
+  if (!std::isfinite(a->scale)) return fail(c, DM0_EINVAL, "the residual scale must be finite");
+  for (int ld : {a->gate_stride, a->mod_stride})
+    if (ld != 0 && (ld < a->hidden || ld % 4 != 0))
+      return fail(c, DM0_EINVAL, "per-sample strides are 0 or at least hidden, multiples of 4");
+  for (const float* p : {a->post_gain, a->pre_gain, a->gate, a->mod_scale, a->mod_shift})
+    if (!aligned16(p)) return fail(c, DM0_EINVAL, "gain, gate and modulation vectors must be 16-byte aligned");
+  return DM0_OK;
+}
+// rows_per_sample collapses to all rows where no vector is per sample
+dm0::RnArgs norm_args(const dm0_ctx* c, const dm0_norm* a) {
+  dm0::RnArgs r{};
+  r.rows = a->batch * a->tokens;
+  r.H = a->hidden;
+  r.gate_ld = a->gate ? a->gate_stride : 0;
+  r.mod_ld = a->mod_scale || a->mod_shift ? a->mod_stride : 0;
+  r.rows_per_sample = r.gate_ld || r.mod_ld ? a->tokens : r.rows;
+  r.alpha = a->scale;
+  r.eps = c->cfg.rms_eps;
+  r.post_gain = a->post_gain;
+  r.pre_gain = a->pre_gain;
+  r.gate = a->gate;
+  r.mod_scale = a->mod_scale;
+  r.mod_shift = a->mod_shift;
+  return r;
+}
+
+template <typename Th, typename Ty>
+dm0_status norm_run(dm0_ctx* c, cudaStream_t s, const dm0::RnArgs& a, const Th* h, const Ty* y, Th* h_out, bf16* n_out,
+                    float* r_post, float* r_pre) {
+  auto go = [&](auto kernel, int warps) {
+    const int rows = 8 / warps;
+    return launch(c, s, kernel, dim3((a.rows + rows - 1) / rows), dim3(256), 0, h, y, a, h_out, n_out, r_post, r_pre);
+  };
+  if (a.H <= 256) return go(dm0::residual_norm_kernel<Th, Ty, 1, 1>, 1);
+  if (a.H <= 512) return go(dm0::residual_norm_kernel<Th, Ty, 2, 1>, 1);
+  if (a.H <= 1024) return go(dm0::residual_norm_kernel<Th, Ty, 4, 1>, 1);
+  if (a.H <= 2048) return go(dm0::residual_norm_kernel<Th, Ty, 8, 1>, 1);
+  if (a.H <= 4096) return go(dm0::residual_norm_kernel<Th, Ty, 8, 2>, 2);
+  return go(dm0::residual_norm_kernel<Th, Ty, 8, 4>, 4);
+}
+
+// Stripes per sample of the backward pass: about four blocks per SM in all, at least one row each.
+int norm_stripes(int samples, int rows_per_sample) {
+  const int want = std::max(1, 4 * kLangSms / samples);
+  return std::min(want, rows_per_sample);
+}
+int norm_samples(const dm0_norm* a) {
+  return (a->gate && a->gate_stride) || ((a->mod_scale || a->mod_shift) && a->mod_stride) ? a->batch : 1;
+}
+size_t norm_grad_bytes(const dm0_norm* a) {
+  const int samples = norm_samples(a), T = samples == 1 ? a->batch * a->tokens : a->tokens;
+  return align256(sizeof(float) * 3 * a->hidden * static_cast<size_t>(samples) * norm_stripes(samples, T));
+}
+
+template <typename Tn, typename Th, typename Ty>
+dm0_status norm_grad_run(dm0_ctx* c, cudaStream_t s, const dm0::RnGradArgs& a, int samples, const Tn* dn,
+                         const Th* dh_out, const Th* h_out, const Ty* y, Th* dh, Ty* dy) {
+  const int threads = (a.f.H / 8 + 31) / 32 * 32;
+  auto go = [&](auto kernel) {
+    return launch(c, s, kernel, dim3(samples * a.stripes), dim3(threads), 0, dn, dh_out, h_out, y, a, dh, dy);
+  };
+  if (threads <= 256) return go(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 256>);
+  return go(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 1024>);
+}
+
+// ---------------------------------------------------------------- vocabulary loss
+constexpr int kVgStages = 4;
+constexpr int kVgPieceElems = 1 << 27;   // entries of G held at a time: 256 MB of workspace
+
+// bf16 [rows][cols] map of 64-column boxes of `box` rows, 128-byte swizzle (nothing is kept by address)
+dm0_status vg_tmap(dm0_ctx* c, CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint32_t box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(c, DM0_ECUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+  cuuint32_t boxd[2] = {64, box}, estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxd, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DM0_OK : fail(c, DM0_ECUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
+}
+
+struct VocabLossPlan {
+  int bn, mt, nt, part_ld;
+  size_t part, zt, bytes;
+};
+VocabLossPlan vocab_loss_plan(int tokens, int vocab) {
+  VocabLossPlan p{};
+  p.mt = (tokens + 127) / 128;
+  p.bn = 256;
+  p.nt = (vocab + p.bn - 1) / p.bn;
+  p.part_ld = (tokens + 31) / 32 * 32;
+  p.part = 0;
+  p.zt = align256(sizeof(float2) * 2 * p.nt * static_cast<size_t>(p.part_ld));
+  p.bytes = p.zt + align256(sizeof(float) * static_cast<size_t>(tokens));
+  return p;
+}
+
+struct VocabGradPlan {
+  int piece, splits, kb_per_split;
+  size_t scale, g, dh, bytes;
+};
+VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
+  VocabGradPlan p{};
+  const int vr = (vocab + 255) / 256 * 256;
+  const int most = std::min(vr, std::max(256, kVgPieceElems / tokens / 256 * 256));
+  const int pieces = (vr + most - 1) / most;
+  p.piece = ((vr + pieces - 1) / pieces + 255) / 256 * 256;
+  // splits of dh's contraction over the piece: whole waves of tiles against the traffic of the fp32 sums
+  const int64_t tiles = static_cast<int64_t>((tokens + 127) / 128) * ((H + 255) / 256);
+  const int KB = (std::min(p.piece, vocab) + 63) / 64;   // of the first piece, whose splits all write
+  double best = 0;
+  for (int S = 1; S <= std::min(KB, 64); ++S) {
+    const int per = (KB + S - 1) / S, used = (KB + per - 1) / per;
+    if (used != S) continue;
+    const double t = static_cast<double>((tiles * S + kLangSms - 1) / kLangSms) * (per * 0.28 + 1.0) +
+                     S * 8.0 * tokens * H / 6.0e6;
+    if (S == 1 || t < best) best = t, p.splits = S, p.kb_per_split = per;
+  }
+  p.scale = 0;
+  p.g = 256;
+  p.dh = p.g + align256(sizeof(bf16) * static_cast<size_t>(tokens) * p.piece);
+  p.bytes = p.dh + align256(sizeof(float) * p.splits * static_cast<size_t>(tokens) * H);
+  return p;
+}
+
+dm0_status vocab_ok(dm0_ctx* c, const void* h, const void* w, const void* t, int tokens, int vocab, int H) {
+  if (!h || !w || !t) return fail(c, DM0_EINVAL, "null argument");
+  if (tokens < 1 || tokens > kLangMaxTokens || vocab < 1 || vocab > kLangMaxVocab)
+    return fail(c, DM0_ESHAPE, "tokens or vocab out of range");
+  if (H < 64 || H % 64 != 0 || H > kLangMaxHidden) return fail(c, DM0_ESHAPE, "hidden must be a multiple of 64");
+  if (!aligned16(h) || !aligned16(w)) return fail(c, DM0_EINVAL, "hidden states and weights must be 16-byte aligned");
+  return DM0_OK;
+}
+
+template <int MODE, int BN>
+dm0_status vocab_gemm(dm0_ctx* c, cudaStream_t s, const CUtensorMap& ta, const CUtensorMap& tb, dm0::VgArgs a) {
+  const int64_t tiles = static_cast<int64_t>(a.mt) * a.nt * a.splits;
+  if (tiles > 0x3fffffff) return fail(c, DM0_ESHAPE, "too many tiles");
+  return launch(c, s, dm0::vocab_gemm_kernel<MODE, BN, kVgStages>,
+                dim3(static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms))), dim3(320),
+                dm0::VgSmem<BN, kVgStages>::kBytes, ta, tb, a);
+}
+
+dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16* w, dm0::Ids tgt, int tokens, int vocab,
+                          int H, float* loss, float* lse, uint8_t* ws) {
+  const VocabLossPlan p = vocab_loss_plan(tokens, vocab);
+  CUtensorMap ta, tb;
+  TRY(vg_tmap(c, &ta, h, tokens, H, 128));
+  TRY(vg_tmap(c, &tb, w, vocab, H, p.bn));
+  dm0::VgArgs a{};
+  a.M = tokens;
+  a.N = vocab;
+  a.K = H;
+  a.mt = p.mt;
+  a.nt = p.nt;
+  a.splits = 1;
+  a.kb_per_split = H / 64;
+  a.err = c->d_err;
+  a.targets = tgt;
+  a.vocab = vocab;
+  a.valid_n = vocab;
+  a.part = reinterpret_cast<float2*>(ws + p.part);
+  a.part_ld = p.part_ld;
+  a.zt = reinterpret_cast<float*>(ws + p.zt);
+  TRY((vocab_gemm<dm0::kVgStats, 256>(c, s, ta, tb, a)));
+  return launch(c, s, dm0::vocab_loss_kernel, dim3((tokens + 31) / 32), dim3(512), 0,
+                static_cast<const float2*>(a.part), 2 * p.nt, p.part_ld, static_cast<const float*>(a.zt), tgt, tokens,
+                vocab, loss, lse, c->d_err);
+}
+
+dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16* w, dm0::Ids tgt, const float* lse,
+                          const float* dloss, int tokens, int vocab, int H, void* dh, int dh_f32, void* dw, int dw_f32,
+                          int accumulate, uint8_t* ws) {
+  const VocabGradPlan p = vocab_grad_plan(tokens, vocab, H);
+  float* scale = reinterpret_cast<float*>(ws + p.scale);
+  bf16* g = reinterpret_cast<bf16*>(ws + p.g);
+  float* part = reinterpret_cast<float*>(ws + p.dh);
+  TRY(launch(c, s, dm0::vocab_scale_kernel, dim3(1), dim3(1024), 0, dloss, tgt, tokens, vocab, scale, c->d_err));
+  CUtensorMap h_k, w_k, g_k, w_mn, g_mn, h_mn;
+  TRY(vg_tmap(c, &h_k, h, tokens, H, 128));
+  TRY(vg_tmap(c, &w_k, w, vocab, H, 256));
+  TRY(vg_tmap(c, &g_k, g, tokens, p.piece, 128));
+  TRY(vg_tmap(c, &w_mn, w, vocab, H, 64));
+  TRY(vg_tmap(c, &g_mn, g, tokens, p.piece, 64));
+  TRY(vg_tmap(c, &h_mn, h, tokens, H, 64));
+  const int mt = (tokens + 127) / 128, ht = (H + 255) / 256;
+  for (int v0 = 0; v0 < vocab; v0 += p.piece) {
+    const int cols = std::min(p.piece, vocab - v0);
+    dm0::VgArgs a{};
+    a.err = c->d_err;
+    a.scale = scale;
+    a.vocab = vocab;
+    a.v0 = v0;
+    // G of the piece
+    a.M = tokens;
+    a.N = cols;
+    a.K = H;
+    a.mt = mt;
+    a.nt = (cols + 255) / 256;
+    a.splits = 1;
+    a.kb_per_split = H / 64;
+    a.b_y0 = v0;
+    a.targets = tgt;
+    a.valid_n = cols;
+    a.lse = lse;
+    a.dloss = dloss;
+    a.g = g;
+    a.ldg = p.piece;
+    TRY((vocab_gemm<dm0::kVgGrad, 256>(c, s, h_k, w_k, a)));
+    if (dh) {
+      a.N = H;
+      a.K = cols;
+      a.nt = ht;
+      a.kb_per_split = p.kb_per_split;
+      a.splits = ((cols + 63) / 64 + p.kb_per_split - 1) / p.kb_per_split;
+      a.band = 1;
+      a.dh = part;
+      a.add = v0 > 0;
+      TRY((vocab_gemm<dm0::kVgHidden, 256>(c, s, g_k, w_mn, a)));
+    }
+    if (dw) {
+      a.M = cols;
+      a.N = H;
+      a.K = tokens;
+      a.mt = (cols + 127) / 128;
+      a.nt = ht;
+      a.splits = 1;
+      a.kb_per_split = (tokens + 63) / 64;
+      a.band = 1;
+      a.b_y0 = 0;
+      a.add = accumulate;
+      a.dw = dw;
+      a.dw_f32 = dw_f32;
+      TRY((vocab_gemm<dm0::kVgWeight, 256>(c, s, g_mn, h_mn, a)));
+    }
+  }
+  if (!dh) return DM0_OK;
+  const int64_t n = static_cast<int64_t>(tokens) * H;
+  const dim3 grid(static_cast<unsigned>((n / 8 + 255) / 256));
+  // the splits of the first piece; the last piece may have used fewer
+  const int splits = p.splits;
+  if (dh_f32)
+    return launch(c, s, dm0::vocab_hidden_kernel<float>, grid, dim3(256), 0, static_cast<const float*>(part), splits, n,
+                  static_cast<const float*>(scale), static_cast<float*>(dh));
+  return launch(c, s, dm0::vocab_hidden_kernel<bf16>, grid, dim3(256), 0, static_cast<const float*>(part), splits, n,
+                static_cast<const float*>(scale), static_cast<bf16*>(dh));
+}
+
+// shared-memory limits of these kernels (dm0_create)
+bool lang_setup() {
+  auto attr = [](auto kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  const int v = dm0::VgSmem<256, kVgStages>::kBytes;
+  return attr(dm0::embed_sort_kernel, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgStats, 256, kVgStages>, v) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgGrad, 256, kVgStages>, v) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgHidden, 256, kVgStages>, v) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgWeight, 256, kVgStages>, v);
+}
+}  // namespace
+
+// Runs a callable with a typed null pointer for each of (fp32, bf16)
+#define DM0_BY_TYPE(f32, T, ...)                \
+  [&]() -> dm0_status {                         \
+    if (f32) {                                  \
+      using T = float;                          \
+      return [&]() -> dm0_status __VA_ARGS__(); \
+    }                                           \
+    using T = bf16;                             \
+    return [&]() -> dm0_status __VA_ARGS__();   \
+  }()
+
+extern "C" {
+
+dm0_status dm0_embed(dm0_ctx* c, const void* table, const void* ids, int ids_i64, int B, int T, int vocab, int hidden,
+                     float scale, void* out, int out_f32, int64_t batch_stride, int64_t row_stride, void* stream) {
+  if (!table || !ids || !out) return fail(c, DM0_EINVAL, "null argument");
+  if (!lang_tokens_ok(B, T) || vocab < 1 || vocab > kLangMaxVocab) return fail(c, DM0_ESHAPE, "bad batch, tokens or vocab");
+  if (hidden < 8 || hidden % 8 != 0 || hidden > kLangMaxHidden)
+    return fail(c, DM0_ESHAPE, "hidden must be a multiple of 8, at most 65536");
+  if (!aligned16(table)) return fail(c, DM0_EINVAL, "the table must be 16-byte aligned");
+  TRY(rows_ok(c, out, out_f32, T, hidden, batch_stride, row_stride));
+  if (B > 1 && batch_stride < (T - 1) * row_stride + hidden && (batch_stride < hidden || row_stride < (B - 1) * batch_stride + hidden))
+    return fail(c, DM0_EINVAL, "the rows of out overlap");
+  TRY(lang_enter(c));
+  const int n = B * T;
+  const dm0::Ids id{ids, ids_i64};
+  const dm0::RowsView v{batch_stride, row_stride, T};
+  return DM0_BY_TYPE(out_f32, To, {
+    return launch(c, static_cast<cudaStream_t>(stream), dm0::embed_kernel<To>, dim3((n + 7) / 8), dim3(256), 0,
+                  static_cast<const bf16*>(table), id, n, vocab, hidden, scale, static_cast<To*>(out), v, c->d_err);
+  });
+}
+
+size_t dm0_embed_grad_workspace(int B, int T, int vocab, int hidden) {
+  if (!lang_tokens_ok(B, T) || vocab < 1 || vocab > kLangMaxVocab || hidden < 8 || hidden > kLangMaxHidden) return 0;
+  return emb_grad_plan(B * T, vocab, hidden).bytes;
+}
+
+dm0_status dm0_embed_grad(dm0_ctx* c, const void* ids, int ids_i64, int B, int T, int vocab, int hidden, float scale,
+                          const void* dout, int dout_f32, int64_t batch_stride, int64_t row_stride, float* grad,
+                          int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ids || !dout || !grad || !workspace) return fail(c, DM0_EINVAL, "null argument");
+  if (!lang_tokens_ok(B, T) || vocab < 1 || vocab > kLangMaxVocab) return fail(c, DM0_ESHAPE, "bad batch, tokens or vocab");
+  if (hidden < 8 || hidden % 8 != 0 || hidden > kLangMaxHidden)
+    return fail(c, DM0_ESHAPE, "hidden must be a multiple of 8, at most 65536");
+  if (!aligned16(grad) || !aligned16(workspace)) return fail(c, DM0_EINVAL, "grad and workspace must be 16-byte aligned");
+  TRY(rows_ok(c, dout, dout_f32, T, hidden, batch_stride, row_stride));
+  if (workspace_bytes < emb_grad_plan(B * T, vocab, hidden).bytes) return fail(c, DM0_EINVAL, "workspace too small");
+  TRY(lang_enter(c));
+  const dm0::Ids id{ids, ids_i64};
+  const dm0::RowsView v{batch_stride, row_stride, T};
+  return DM0_BY_TYPE(dout_f32, Td, {
+    return embed_grad_run(c, static_cast<cudaStream_t>(stream), id, B * T, v, vocab, hidden, scale,
+                          static_cast<const Td*>(dout), grad, accumulate, static_cast<uint8_t*>(workspace));
+  });
+}
+
+dm0_status dm0_residual_norm(dm0_ctx* c, const dm0_norm* a, const void* h, const void* y, void* h_out, void* n_out,
+                             float* r_post, float* r_pre, void* stream) {
+  TRY(norm_ok(c, a));
+  if (!h || !h_out || !n_out || !r_pre || (y && a->post_gain && !r_post)) return fail(c, DM0_EINVAL, "null argument");
+  if (!y && (a->post_gain || a->gate)) return fail(c, DM0_EINVAL, "a post gain or gate needs a block output");
+  for (const void* p : {h, y, static_cast<const void*>(h_out), static_cast<const void*>(n_out)})
+    if (!aligned16(p)) return fail(c, DM0_EINVAL, "row tensors must be 16-byte aligned");
+  TRY(lang_enter(c));
+  const dm0::RnArgs r = norm_args(c, a);
+  return DM0_BY_TYPE(a->h_f32, Th, {
+    return DM0_BY_TYPE(a->y_f32, Ty, {
+      return norm_run(c, static_cast<cudaStream_t>(stream), r, static_cast<const Th*>(h), static_cast<const Ty*>(y),
+                      static_cast<Th*>(h_out), static_cast<bf16*>(n_out), r_post, r_pre);
+    });
+  });
+}
+
+size_t dm0_residual_norm_grad_workspace(const dm0_norm* a) {
+  return norm_ok(nullptr, a) == DM0_OK ? norm_grad_bytes(a) : 0;
+}
+
+dm0_status dm0_residual_norm_grad(dm0_ctx* c, const dm0_norm* a, const void* dn, int dn_f32, const void* dh_out,
+                                  const void* h_out, const void* y, const float* r_post, const float* r_pre, void* dh,
+                                  void* dy, const dm0_norm_grads* g, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  TRY(norm_ok(c, a));
+  if (!dn || !h_out || !r_pre || !dh || !g || !workspace || (y && (!dy || (a->post_gain && !r_post))))
+    return fail(c, DM0_EINVAL, "null argument");
+  if (!y && (a->post_gain || a->gate)) return fail(c, DM0_EINVAL, "a post gain or gate needs a block output");
+  if ((g->post_gain && !a->post_gain) || (g->pre_gain && !a->pre_gain) || (g->gate && !a->gate) ||
+      (g->mod_scale && !a->mod_scale) || (g->mod_shift && !a->mod_shift))
+    return fail(c, DM0_EINVAL, "a gradient was asked for a vector that is not there");
+  for (const void* p : {dn, dh_out, h_out, y, static_cast<const void*>(dh), static_cast<const void*>(dy),
+                        static_cast<const void*>(workspace)})
+    if (!aligned16(p)) return fail(c, DM0_EINVAL, "row tensors and workspace must be 16-byte aligned");
+  if (workspace_bytes < norm_grad_bytes(a)) return fail(c, DM0_EINVAL, "workspace too small");
+  TRY(lang_enter(c));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int samples = norm_samples(a);
+  const bool sums = g->post_gain || g->pre_gain || g->gate || g->mod_scale || g->mod_shift;
+  dm0::RnGradArgs r{};
+  r.f = norm_args(c, a);
+  r.r_post = r_post;
+  r.r_pre = r_pre;
+  r.stripes = norm_stripes(samples, r.f.rows_per_sample);
+  r.part = sums ? static_cast<float*>(workspace) : nullptr;
+  TRY(DM0_BY_TYPE(dn_f32, Tn, {
+    return DM0_BY_TYPE(a->h_f32, Th, {
+      return DM0_BY_TYPE(a->y_f32, Ty, {
+        return norm_grad_run(c, s, r, samples, static_cast<const Tn*>(dn), static_cast<const Th*>(dh_out),
+                             static_cast<const Th*>(h_out), static_cast<const Ty*>(y), static_cast<Th*>(dh),
+                             static_cast<Ty*>(dy));
+      });
+    });
+  }));
+  if (!sums) return DM0_OK;
+  dm0::RnSumArgs t{};
+  t.f = r.f;
+  t.samples = samples;
+  t.stripes = r.stripes;
+  t.part = r.part;
+  t.d_post = g->post_gain;
+  t.d_gate = g->gate;
+  t.d_pre = g->pre_gain;
+  t.d_scale = g->mod_scale;
+  t.d_shift = g->mod_shift;
+  return launch(c, s, dm0::residual_norm_sum_kernel, dim3((a->hidden + 31) / 32), dim3(1024), 0, t);
+}
+
+size_t dm0_vocab_loss_workspace(int tokens, int vocab, int hidden) {
+  if (tokens < 1 || tokens > kLangMaxTokens || vocab < 1 || vocab > kLangMaxVocab || hidden < 64) return 0;
+  return vocab_loss_plan(tokens, vocab).bytes;
+}
+
+dm0_status dm0_vocab_loss(dm0_ctx* c, const void* hidden_states, const void* weight, const void* targets,
+                          int targets_i64, int tokens, int vocab, int hidden, float* loss, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  TRY(vocab_ok(c, hidden_states, weight, targets, tokens, vocab, hidden));
+  if (!loss || !lse || !workspace) return fail(c, DM0_EINVAL, "null argument");
+  if (!aligned16(workspace)) return fail(c, DM0_EINVAL, "the workspace must be 16-byte aligned");
+  if (workspace_bytes < vocab_loss_plan(tokens, vocab).bytes) return fail(c, DM0_EINVAL, "workspace too small");
+  TRY(lang_enter(c));
+  return vocab_loss_run(c, static_cast<cudaStream_t>(stream), static_cast<const bf16*>(hidden_states),
+                        static_cast<const bf16*>(weight), dm0::Ids{targets, targets_i64}, tokens, vocab, hidden, loss,
+                        lse, static_cast<uint8_t*>(workspace));
+}
+
+size_t dm0_vocab_loss_grad_workspace(int tokens, int vocab, int hidden) {
+  if (tokens < 1 || tokens > kLangMaxTokens || vocab < 1 || vocab > kLangMaxVocab || hidden < 64 ||
+      hidden > kLangMaxHidden)
+    return 0;
+  return vocab_grad_plan(tokens, vocab, hidden).bytes;
+}
+
+dm0_status dm0_vocab_loss_grad(dm0_ctx* c, const void* hidden_states, const void* weight, const void* targets,
+                               int targets_i64, const float* lse, const float* dloss, int tokens, int vocab, int hidden,
+                               void* dhidden, int dhidden_f32, void* dweight, int dweight_f32, int accumulate,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  TRY(vocab_ok(c, hidden_states, weight, targets, tokens, vocab, hidden));
+  if (!lse || !dloss || !workspace || (!dhidden && !dweight)) return fail(c, DM0_EINVAL, "null argument");
+  if (!aligned16(dhidden) || !aligned16(dweight) || !aligned16(workspace))
+    return fail(c, DM0_EINVAL, "gradients and workspace must be 16-byte aligned");
+  if (accumulate && dweight && !dweight_f32)
+    return fail(c, DM0_EINVAL, "only an fp32 weight gradient accumulates: a bf16 sum would be rounded at every call");
+  if (workspace_bytes < vocab_grad_plan(tokens, vocab, hidden).bytes) return fail(c, DM0_EINVAL, "workspace too small");
+  TRY(lang_enter(c));
+  return vocab_grad_run(c, static_cast<cudaStream_t>(stream), static_cast<const bf16*>(hidden_states),
+                        static_cast<const bf16*>(weight), dm0::Ids{targets, targets_i64}, lse, dloss, tokens, vocab,
+                        hidden, dhidden, dhidden_f32, dweight, dweight_f32, accumulate,
+                        static_cast<uint8_t*>(workspace));
+}
+
+}  // extern "C"
+#undef DM0_BY_TYPE

@@ -1,0 +1,439 @@
+// Softmax cross entropy over a vocabulary, without keeping the logits, and its gradient.
+//
+//   z_iv = h_i . W_v                     lse_i = log sum_v exp(z_iv)
+//   loss_i = lse_i - z_{i, t_i}          (0 where t_i < 0)
+//   G_iv = (exp(z_iv - lse_i) - [v = t_i]) dloss_i      dh = G W      dW = G^T h
+//
+// One tcgen05 kernel does all four products; its mode sets the operands' majors and the epilogue:
+//   kVgStats  z tile -> the row's (max, sum of exp) of its columns, and z_{i, t_i}
+//   kVgGrad   z tile again -> G / s in bf16, one piece of the vocabulary at a time
+//   kVgHidden dh += G W   of the piece: A = G (K-major), B = W read along H (MN-major), fp32 sums
+//   kVgWeight dW  = G^T h of the piece: A = G read along V (MN-major), B = h read along H (MN-major)
+//
+// s = max |dloss_i| over the tokens with a target: G / s is what is rounded to bf16 and s multiplies the
+// fp32 results, so the factor 1 / tokens of a mean, the same in every row, takes no part in the rounding
+// (a constant dloss that is no power of two would otherwise put one and the same relative error of up to
+// 2^-8 / 2 into every entry -dloss of the targets, which no sum averages out).
+//
+// The products are bound by the tensor cores for many tokens and by one read of W for few.
+#pragma once
+#include "attention_tc.cuh"   // sw128_mnmajor_desc
+#include "embedding.cuh"
+#include "gemm.cuh"           // band_tile, resid_swz, bf2
+
+namespace dm0 {
+
+enum VgMode : int { kVgStats = 0, kVgGrad = 1, kVgHidden = 2, kVgWeight = 3 };
+
+struct VgArgs {
+  int M, N, K;          // of this product (rows of A, rows of B, contraction)
+  int mt, nt, splits, kb_per_split;
+  int band;             // raster: m-tiles per band (1: n fastest)
+  int b_y0;             // offset of B's first row in its map: vocabulary row of the piece
+  int* err;
+  // statistics and G
+  Ids targets;
+  int vocab, v0;        // whole vocabulary; first column of the piece
+  int valid_n;          // columns of this product that are vocabulary entries
+  float2* part;         // [2 nt][part_ld] (max, sum) of each tile half
+  int part_ld;
+  float* zt;            // [tokens] logit of the target
+  const float *lse, *dloss, *scale;   // scale[0] = s
+  __nv_bfloat16* g;     // [tokens][ldg]
+  int ldg;
+  // dh: fp32 sums of the splits, [split][tokens][H]; dW: rows of the piece
+  float* dh;
+  int add;              // add to what is there (dh: from the second piece on; dW: accumulate)
+  void* dw;             // [vocab][H]
+  int dw_f32;
+};
+
+template <int BN, int STAGES>
+struct VgSmem {
+  static constexpr uint32_t kA = 128 * 128, kB = BN * 128, kStage = kA + kB, kPipe = STAGES * kStage;
+  static constexpr uint32_t kScr = kPipe;                 // 8 x 4 KB
+  static constexpr uint32_t kBar = kScr + 8 * 4096;
+  static constexpr uint32_t kBytes = kBar + 256 + 1024;   // barriers, alignment slack
+  static_assert(kBytes <= 232448, "shared memory of one CTA");
+};
+
+// 32 rows x 64 bf16 (values of one lane: its row's 64 columns) through the warp's scratch, to rows of
+// `dst` that are `ld` elements apart; 4 whole 128-byte row pieces per store instruction
+__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&lo)[32], const float (&hi)[32],
+                                              __nv_bfloat16* dst, int64_t ld, int rows) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    *reinterpret_cast<uint4*>(scr + resid_swz(lane, j)) =
+        make_uint4(bf2(lo[8 * j], lo[8 * j + 1]), bf2(lo[8 * j + 2], lo[8 * j + 3]), bf2(lo[8 * j + 4], lo[8 * j + 5]),
+                   bf2(lo[8 * j + 6], lo[8 * j + 7]));
+    *reinterpret_cast<uint4*>(scr + resid_swz(lane, j + 4)) =
+        make_uint4(bf2(hi[8 * j], hi[8 * j + 1]), bf2(hi[8 * j + 2], hi[8 * j + 3]), bf2(hi[8 * j + 4], hi[8 * j + 5]),
+                   bf2(hi[8 * j + 6], hi[8 * j + 7]));
+  }
+  __syncwarp();
+  const int qr = lane >> 3, qc = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + qr;
+    if (r < rows)
+      *reinterpret_cast<uint4*>(dst + r * ld + qc * 8) = *reinterpret_cast<const uint4*>(scr + resid_swz(r, qc));
+  }
+  __syncwarp();
+}
+// 32 rows x 32 fp32, added to what is there if `add`
+__device__ __forceinline__ void vg_store_f32(uint8_t* scr, const float (&v)[32], float* dst, int64_t ld, int rows,
+                                             bool add) {
+  const int lane = threadIdx.x & 31;
+  const int qr = lane >> 3, qc = lane & 7;
+  float4 old[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + qr;
+    old[i] = add && r < rows ? *reinterpret_cast<const float4*>(dst + r * ld + qc * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<float4*>(scr + resid_swz(lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + qr;
+    float4 x = *reinterpret_cast<const float4*>(scr + resid_swz(r, qc));
+    if (add) x = make_float4(x.x + old[i].x, x.y + old[i].y, x.z + old[i].z, x.w + old[i].w);
+    if (r < rows) *reinterpret_cast<float4*>(dst + r * ld + qc * 4) = x;
+  }
+  __syncwarp();
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Warp 0: TMA; warp 1: TMEM and MMA; warps 2..9: epilogue, two per TMEM lane quarter (column halves).
+// Persistent: one CTA per SM walks the tiles; the accumulator is double-buffered.
+template <int MODE, int BN, int STAGES>
+__global__ void __launch_bounds__(320, 1)
+    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const VgArgs a) {
+  using L = VgSmem<BN, STAGES>;
+  constexpr bool kAMn = MODE == kVgWeight, kBMn = MODE == kVgHidden || MODE == kVgWeight;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = (a.K + 63) >> 6;
+  const int plane = a.mt * a.nt, ntiles = plane * a.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 2 * BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  auto tile_at = [&](int t, int& m, int& n, int& kb0, int& kb1, int& split) {
+    split = t / plane;
+    band_tile(t - split * plane, a.mt, a.nt, a.band, m, n);
+    kb0 = split * a.kb_per_split;
+    kb1 = min(KB, kb0 + a.kb_per_split);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+      const uint64_t keep = policy_evict_last();
+      int it = 0;
+      for (int t = blockIdx.x; t < ntiles && !*abort_flag; t += gridDim.x) {
+        int m, n, kb0, kb1, split;
+        tile_at(t, m, n, kb0, kb1, split);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (it >= STAGES && !mbar_wait(&empty[s], ((it / STAGES) - 1) & 1, abort_flag)) {
+            *abort_flag = 1;
+            raise_error(a.err, kErrTimeoutProducer);
+            break;
+          }
+          uint8_t* sa = smem + s * L::kStage;
+          uint8_t* sb = sa + L::kA;
+          mbar_arrive_expect_tx(&full[s], L::kStage);
+          if constexpr (kAMn) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) tma_load_2d(sa + 8192 * j, &tmA, &full[s], m * 128 + 64 * j, kb * 64, keep);
+          } else {
+            tma_load_2d(sa, &tmA, &full[s], kb * 64, m * 128, keep);
+          }
+          if constexpr (kBMn) {
+#pragma unroll
+            for (int j = 0; j < BN / 64; ++j)
+              tma_load_2d(sb + 8192 * j, &tmB, &full[s], n * BN + 64 * j, a.b_y0 + kb * 64, keep);
+          } else {
+            tma_load_2d(sb, &tmB, &full[s], kb * 64, a.b_y0 + n * BN, keep);
+          }
+        }
+      }
+      for (int i = it - STAGES; i < it; ++i) {   // copies in flight land before the CTA exits
+        if (i < 0) continue;
+        if (!mbar_wait(&full[i % STAGES], (i / STAGES) & 1, nullptr, kDrainTimeoutNs)) raise_error(a.err, kErrDrain);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(128, BN) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+      int it = 0, local = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++local) {
+        int m, n, kb0, kb1, split;
+        tile_at(t, m, n, kb0, kb1, split);
+        const int buf = local & 1;
+        if (local >= 2 && !mbar_wait(&tempty[buf], ((local >> 1) - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(&full[s], (it / STAGES) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t aa = smem_u32(smem + s * L::kStage), bb = aa + L::kA;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t da = kAMn ? sw128_mnmajor_desc(aa + 2048 * kk, 8192) : sw128_kmajor_desc(aa + 32 * kk);
+            const uint64_t db = kBMn ? sw128_mnmajor_desc(bb + 2048 * kk, 8192) : sw128_kmajor_desc(bb + 32 * kk);
+            umma_bf16(tmem + buf * BN, da, db, idesc, (kb > kb0 || kk != 0) ? 1u : 0u);
+          }
+          umma_commit(&empty[s]);
+        }
+        if (ok) umma_commit(&tfull[buf]);
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        raise_error(a.err, kErrTimeoutMma);
+      }
+      umma_commit(drain);
+      if (!mbar_wait(drain, 0, nullptr, kWaitTimeoutNs + kDrainTimeoutNs)) raise_error(a.err, kErrDrain);
+    }
+  } else {
+    const int lane_base = (warp & 3) * 32, half = (warp - 2) >> 2;
+    uint8_t* scr = smem + L::kScr + (warp - 2) * 4096;
+    constexpr int kCols = BN / 2;   // columns of this warp
+    const float s = MODE == kVgGrad || MODE == kVgWeight ? a.scale[0] : 1.f;
+    int local = 0;
+    for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++local) {
+      int m, n, kb0, kb1, split;
+      tile_at(t, m, n, kb0, kb1, split);
+      const int buf = local & 1;
+      if (!mbar_wait(&tfull[buf], (local >> 1) & 1, abort_flag)) {
+        *abort_flag = 1;
+        raise_error(a.err, kErrTimeoutEpilogue);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tm = tmem + (static_cast<uint32_t>(lane_base) << 16) + buf * BN + half * kCols;
+      const int row0 = m * 128 + lane_base, row = row0 + lane;
+      const int col0 = n * BN + half * kCols;
+      const int rows = min(32, a.M - row0);   // rows of this warp to store (may be <= 0)
+      if constexpr (MODE == kVgStats) {
+        const int tgt = row < a.M ? a.targets.get(row) : -1;
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < kCols / 32; ++c) {
+          float v[32];
+          tmem_ld32(tm + 32 * c, v);
+          const int cc = col0 + 32 * c;
+          if (cc + 32 > a.valid_n) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (cc + j >= a.valid_n) v[j] = -INFINITY;
+          }
+          float cm = mx;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) cm = max3f(cm, v[j], v[j + 1]);
+          const float ref = cm == -INFINITY ? 0.f : cm * kLog2e;
+          float acc = sum * ex2_fast(mx * kLog2e - ref);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc += ex2_fast(fmaf(v[j], kLog2e, -ref));
+          sum = acc;
+          mx = cm;
+          const unsigned at = static_cast<unsigned>(tgt - cc);
+          if (tgt >= 0 && at < 32u && tgt < a.vocab) {
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z = at == static_cast<unsigned>(j) ? v[j] : z;
+            a.zt[row] = z;
+          }
+        }
+        if (row < a.M) a.part[static_cast<int64_t>(2 * n + half) * a.part_ld + row] = make_float2(mx, sum);
+      } else if constexpr (MODE == kVgGrad) {
+        int tgt = -1;
+        float l2 = 0.f, gi = 0.f;
+        if (row < a.M) {
+          tgt = a.targets.get(row);
+          if (tgt >= a.vocab) tgt = -1;
+          l2 = a.lse[row] * kLog2e;
+          gi = a.dloss[row] / s;
+        }
+        const int rel = tgt - a.v0;   // column of the target in this piece (maybe outside)
+#pragma unroll 1
+        for (int c = 0; c < kCols / 64; ++c) {
+          float v[2][32];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            tmem_ld32(tm + 64 * c + 32 * q, v[q]);
+            const int cc = col0 + 64 * c + 32 * q;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[q][j] = ex2_fast(fmaf(v[q][j], kLog2e, -l2)) * gi;
+            if (static_cast<unsigned>(rel - cc) < 32u) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (rel - cc == j) v[q][j] -= gi;
+            }
+            if (tgt < 0 || cc + 32 > a.valid_n) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (tgt < 0 || cc + j >= a.valid_n) v[q][j] = 0.f;
+            }
+          }
+          vg_store_bf16(scr, v[0], v[1], a.g + static_cast<int64_t>(row0) * a.ldg + col0 + 64 * c, a.ldg, rows);
+        }
+      } else if constexpr (MODE == kVgHidden) {
+        float* dst = a.dh + (static_cast<int64_t>(split) * a.M + row0) * a.N + col0;
+#pragma unroll 1
+        for (int c = 0; c < kCols / 32; ++c) {
+          float v[32];
+          tmem_ld32(tm + 32 * c, v);
+          if (col0 + 32 * c < a.N) vg_store_f32(scr, v, dst + 32 * c, a.N, rows, a.add != 0);
+        }
+      } else {
+        const int64_t at = static_cast<int64_t>(a.v0 + row0) * a.N + col0;
+#pragma unroll 1
+        for (int c = 0; c < kCols / 64; ++c) {
+          float v[2][32];
+          tmem_ld32(tm + 64 * c, v[0]);
+          tmem_ld32(tm + 64 * c + 32, v[1]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[q][j] *= s;
+          if (col0 + 64 * c >= a.N) continue;
+          if (a.dw_f32) {
+            float* dst = static_cast<float*>(a.dw) + at + 64 * c;
+            vg_store_f32(scr, v[0], dst, a.N, rows, a.add != 0);
+            vg_store_f32(scr, v[1], dst + 32, a.N, rows, a.add != 0);
+          } else {
+            vg_store_bf16(scr, v[0], v[1], static_cast<__nv_bfloat16*>(a.dw) + at + 64 * c, a.N, rows);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * BN);
+  }
+}
+
+// The tiles' (max, sum) of 32 tokens joined: 16 lanes of tiles per token, then the lanes in order.
+__global__ void __launch_bounds__(512) vocab_loss_kernel(const float2* part, int parts, int part_ld, const float* zt,
+                                                         Ids targets, int tokens, int vocab, float* loss, float* lse,
+                                                         int* err) {
+  pdl_wait();
+  __shared__ float2 red[16][32];
+  const int tl = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + tl;
+  const bool in = i < tokens;
+  float mx = -INFINITY, sum = 0.f;
+  auto join = [&](float2 p) {
+    const float m = fmaxf(mx, p.x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    sum = sum * expf(mx - ref) + p.y * expf(p.x - ref);
+    mx = m;
+  };
+  if (in) {
+#pragma unroll 8
+    for (int p = g; p < parts; p += 16) join(part[static_cast<int64_t>(p) * part_ld + i]);
+  }
+  red[g][tl] = make_float2(mx, sum);
+  __syncthreads();
+  if (g != 0 || !in) return;
+  for (int k = 1; k < 16; ++k) join(red[k][tl]);
+  const float l = mx + logf(sum);
+  const int t = targets.get(i);
+  if (t >= vocab) raise_error(err, kErrBounds);
+  lse[i] = l;
+  loss[i] = t >= 0 && t < vocab ? l - zt[i] : 0.f;
+}
+
+// s of the header comment: max |dloss| over the tokens with a target, 1 if that is 0
+__global__ void __launch_bounds__(1024) vocab_scale_kernel(const float* dloss, Ids targets, int tokens, int vocab,
+                                                           float* scale, int* err) {
+  pdl_wait();
+  __shared__ float red[32];
+  float m = 0.f;
+  bool bad = false;
+  for (int i = threadIdx.x; i < tokens; i += blockDim.x) {
+    const int t = targets.get(i);
+    bad |= t >= vocab;
+    if (t >= 0 && t < vocab) m = fmaxf(m, fabsf(dloss[i]));
+  }
+  if (bad) raise_error(err, kErrBounds);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 32; ++k) m = fmaxf(m, red[k]);
+    scale[0] = m > 0.f ? m : 1.f;
+  }
+}
+
+// dh = s * the sum of the splits, in order
+template <typename To>
+__global__ void __launch_bounds__(256) vocab_hidden_kernel(const float* part, int splits, int64_t n, const float* scale,
+                                                           To* dh) {
+  pdl_wait();
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  const float s = scale[0];
+  float f[8] = {};
+  for (int k = 0; k < splits; ++k) {
+    float p[8];
+    load8_rw(part + k * n + i, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += p[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] *= s;
+  store8(dh + i, f);
+}
+
+}  // namespace dm0
