@@ -10,8 +10,9 @@ import ctypes
 
 import numpy as np
 
-from ._abi import (EXPORTS, LIB_PATH, SITES, Dm0Config, Dm0Error, Dm0Norm, Dm0NormGrads,  # noqa: F401
-                   load_library, make_config, pack_weights)
+from ._abi import (EXPORTS, LIB_PATH, SITES, Dm0Config, Dm0Error, load_library, make_config,  # noqa: F401
+                   pack_weights)
+from .language import LanguageOps
 
 __all__ = ["Engine", "Dm0Error", "pack_weights", "pack_e4m3_rows", "load_library", "EXPORTS", "LIB_PATH"]
 
@@ -38,26 +39,6 @@ def _check_cuda(t, dtype, shape, name):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _check_on(t, device, dtypes, shape, name):
-    """A contiguous tensor of `shape` and one of `dtypes` on CUDA device `device` (the context's)."""
-    if not (t.is_cuda and t.get_device() == device and t.dtype in dtypes and t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous tensor on cuda:{device} of {' or '.join(map(str, dtypes))}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _check_rows(t, device, dtypes, shape, name):
-    """As _check_on for [T][H] or [B][T][H] rows that are contiguous themselves: (batch stride, row stride)."""
-    if not (t.is_cuda and t.get_device() == device and t.dtype in dtypes):
-        raise TypeError(f"{name} must be a tensor on cuda:{device} of {' or '.join(map(str, dtypes))}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    # the stride of a dimension of one says nothing
-    return (t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else 0), (t.stride(-2) if t.shape[-2] > 1 else t.shape[-1])
-
-
 def pack_e4m3_rows(x: np.ndarray):
     """FP8 E4M3 codes (uint8, OCP bit patterns) and one fp32 scale per row of a 2-D array, through
     dm0_pack_e4m3_rows (host code; no GPU needed)."""
@@ -73,7 +54,7 @@ def pack_e4m3_rows(x: np.ndarray):
     return codes, scales
 
 
-class Engine:
+class Engine(LanguageOps):
     """One dm0_ctx on the current CUDA device."""
 
     def __init__(self, dims, max_batch: int, max_prefix: int, time_mod: bool = False):
@@ -87,8 +68,7 @@ class Engine:
         if st != 0 or not h.value:
             raise Dm0Error(st, "dm0_create failed (configuration or device allocation)")
         self.h = h
-        import torch
-        self.device = torch.cuda.current_device()   # the context's: tensors of the language operators live there
+        self._open_language()
 
     # ------------------------------------------------------------------ helpers
     def _chk(self, st: int):
@@ -245,199 +225,6 @@ class Engine:
         Tb = 0 if kb is None else kb.shape[2]
         self._chk(self.lib.dm0_op_attention(self.h, _ptr(q), _ptr(ka), _ptr(va), Ta, _ptr(kb), _ptr(vb), Tb,
                                             _ptr(o), B, Tq, splits, _stream(stream)))
-
-    # ------------------------------------------------------------------ language side
-    def _ids(self, ids, name):
-        import torch
-        if ids.dim() not in (1, 2):
-            raise ValueError(f"{name} must be [T] or [B][T]")
-        _check_on(ids, self.device, (torch.int64, torch.int32), ids.shape, name)
-        return ids.dtype == torch.int64, (1 if ids.dim() == 1 else ids.shape[0]), ids.shape[-1]
-
-    def embed(self, table, ids, scale: float = 1.0, out=None, stream=None):
-        """scale * table[ids] (dm0_embed), a zero row where an id is negative.
-
-        table: CUDA bf16 [vocab][hidden]; ids: int32 or int64 [T] or [B][T]; out (bf16, made if not given, or fp32):
-        [T][hidden] or [B][T][hidden], whose rows are contiguous but may lie apart, as the text rows behind the
-        image rows of a prefix do: out=prefix_emb[:, image_rows:]."""
-        import torch
-        wide, B, T = self._ids(ids, "ids")
-        if table.dim() != 2:
-            raise ValueError("table must be [vocab][hidden]")
-        V, H = table.shape
-        _check_on(table, self.device, (torch.bfloat16,), table.shape, "table")
-        shape = (*ids.shape, H)
-        if out is None:
-            out = torch.empty(shape, device=table.device, dtype=torch.bfloat16)
-        bs, rs = _check_rows(out, self.device, (torch.bfloat16, torch.float32), shape, "out")
-        self._chk(self.lib.dm0_embed(self.h, _ptr(table), _ptr(ids), wide, B, T, V, H, scale, _ptr(out),
-                                     out.dtype == torch.float32, bs, rs, _stream(stream)))
-        return out
-
-    def embed_grad(self, ids, dout, vocab: int, scale: float = 1.0, grad=None, accumulate: bool = False, stream=None):
-        """Gradient of embed with respect to its table (dm0_embed_grad): f32 [vocab][hidden].
-
-        dout: bf16 or fp32 rows as embed's out.  accumulate adds to `grad`, e.g. to the weight gradient that
-        vocab_loss_grad left there when the loss's weights are the table."""
-        import torch
-        wide, B, T = self._ids(ids, "ids")
-        H = dout.shape[-1]
-        bs, rs = _check_rows(dout, self.device, (torch.bfloat16, torch.float32), (*ids.shape, H), "dout")
-        if grad is None:
-            if accumulate:
-                raise ValueError("accumulate needs grad")
-            grad = torch.empty((vocab, H), device=dout.device, dtype=torch.float32)
-        _check_on(grad, self.device, (torch.float32,), (vocab, H), "grad")
-        ws = self._workspace(self.lib.dm0_embed_grad_workspace(B, T, vocab, H), stream)
-        self._chk(self.lib.dm0_embed_grad(self.h, _ptr(ids), wide, B, T, vocab, H, scale, _ptr(dout),
-                                          dout.dtype == torch.float32, bs, rs, _ptr(grad), accumulate, _ptr(ws),
-                                          ws.numel(), _stream(stream)))
-        return grad
-
-    def _workspace(self, nbytes: int, stream):
-        """Scratch of one call, from torch's allocator, which keeps it from others until the call's stream is past it."""
-        import torch
-        ws = torch.empty(max(nbytes, 16), device=f"cuda:{self.device}", dtype=torch.uint8)
-        if stream is not None:
-            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                             torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), self.device))
-        return ws
-
-    def _norm(self, h, y, post_gain, gate, scale, pre_gain, mod_scale, mod_shift):
-        import torch
-        two = (torch.float32, torch.bfloat16)
-        if h.dim() not in (2, 3):
-            raise ValueError("the residual stream must be [T][hidden] or [B][T][hidden]")
-        B, T, H = (1, *h.shape) if h.dim() == 2 else h.shape
-        _check_on(h, self.device, two, h.shape, "the residual stream")
-        if y is not None:
-            _check_on(y, self.device, two, h.shape, "y")
-        for v, name in ((post_gain, "post_gain"), (pre_gain, "pre_gain")):
-            if v is not None:
-                _check_on(v, self.device, (torch.float32,), (H,), name)
-        strides = {}
-        for v, name in ((gate, "gate"), (mod_scale, "mod_scale"), (mod_shift, "mod_shift")):
-            strides[name] = 0
-            if v is None:
-                continue
-            if not (v.is_cuda and v.get_device() == self.device and v.dtype == torch.float32 and v.stride(-1) == 1):
-                raise TypeError(f"{name} must be an fp32 tensor on cuda:{self.device} with contiguous rows")
-            if v.shape != (H,) and v.shape != (B, H):
-                raise ValueError(f"{name} has shape {tuple(v.shape)}, expected {(H,)} or {(B, H)}")
-            strides[name] = v.stride(0) if v.dim() == 2 and B > 1 else 0
-            if v.dim() == 2 and B > 1 and v.stride(0) < H:
-                raise ValueError(f"the rows of {name} overlap")
-        if mod_scale is not None and mod_shift is not None and strides["mod_scale"] != strides["mod_shift"]:
-            raise ValueError("mod_scale and mod_shift must be laid out alike")
-        return Dm0Norm(B, T, H, h.dtype == torch.float32, y is not None and y.dtype == torch.float32, scale,
-                       _ptr(post_gain), _ptr(gate), strides["gate"], _ptr(pre_gain), _ptr(mod_scale),
-                       _ptr(mod_shift), max(strides["mod_scale"], strides["mod_shift"]))
-
-    def residual_norm(self, h, y=None, post_gain=None, gate=None, scale: float = 1.0, pre_gain=None, mod_scale=None,
-                      mod_shift=None, h_out=None, n_out=None, stream=None):
-        """The boundary behind a block (dm0_residual_norm): norm of its output y, gate, scaled residual and the next
-        block's norm, in one pass.
-
-        h, y: bf16 or fp32 [T][hidden] or [B][T][hidden]; gains f32 [hidden]; gate, mod_scale, mod_shift f32 [hidden]
-        or [B][hidden].  Returns (h_out, n_out bf16, r_post or None, r_pre); the last two are the rows' 1 / rms for
-        residual_norm_grad."""
-        import torch
-        a = self._norm(h, y, post_gain, gate, scale, pre_gain, mod_scale, mod_shift)
-        if h_out is None:
-            h_out = torch.empty_like(h)
-        if n_out is None:
-            n_out = torch.empty_like(h, dtype=torch.bfloat16)
-        _check_on(h_out, self.device, (h.dtype,), h.shape, "h_out")
-        _check_on(n_out, self.device, (torch.bfloat16,), h.shape, "n_out")
-        r_pre = torch.empty(h.shape[:-1], device=h.device, dtype=torch.float32)
-        r_post = torch.empty_like(r_pre) if post_gain is not None else None
-        self._chk(self.lib.dm0_residual_norm(self.h, ctypes.byref(a), _ptr(h), _ptr(y), _ptr(h_out), _ptr(n_out),
-                                             _ptr(r_post), _ptr(r_pre), _stream(stream)))
-        return h_out, n_out, r_post, r_pre
-
-    def residual_norm_grad(self, dn, dh_out, h_out, y, r_post, r_pre, post_gain=None, gate=None, scale: float = 1.0,
-                           pre_gain=None, mod_scale=None, mod_shift=None, stream=None) -> dict:
-        """Adjoint of residual_norm (dm0_residual_norm_grad), from its outputs and the gradients dn (bf16 or fp32) of
-        n_out and dh_out (the residual's type, or None) of h_out.
-
-        Returns a dict: "h", "y" (their types) and, for each vector that was given, its f32 gradient ("post_gain",
-        "gate", "pre_gain", "mod_scale", "mod_shift"), of the vector's shape."""
-        import torch
-        a = self._norm(h_out, y, post_gain, gate, scale, pre_gain, mod_scale, mod_shift)
-        _check_on(dn, self.device, (torch.bfloat16, torch.float32), h_out.shape, "dn")
-        if dh_out is not None:
-            _check_on(dh_out, self.device, (h_out.dtype,), h_out.shape, "dh_out")
-        for r, name in ((r_pre, "r_pre"), (r_post, "r_post")):
-            if r is not None:
-                _check_on(r, self.device, (torch.float32,), h_out.shape[:-1], name)
-        out = {"h": torch.empty_like(h_out)}
-        if y is not None:
-            out["y"] = torch.empty_like(y)
-        vecs = {"post_gain": post_gain, "gate": gate, "pre_gain": pre_gain, "mod_scale": mod_scale,
-                "mod_shift": mod_shift}
-        out.update((k, torch.empty(v.shape, device=v.device, dtype=torch.float32)) for k, v in vecs.items()
-                   if v is not None)
-        g = Dm0NormGrads(*(_ptr(out.get(k)) for k in vecs))
-        ws = self._workspace(self.lib.dm0_residual_norm_grad_workspace(ctypes.byref(a)), stream)
-        self._chk(self.lib.dm0_residual_norm_grad(
-            self.h, ctypes.byref(a), _ptr(dn), dn.dtype == torch.float32, _ptr(dh_out), _ptr(h_out), _ptr(y),
-            _ptr(r_post), _ptr(r_pre), _ptr(out["h"]), _ptr(out.get("y")), ctypes.byref(g), _ptr(ws), ws.numel(),
-            _stream(stream)))
-        return out
-
-    def _vocab(self, hidden, weight, targets):
-        import torch
-        if hidden.dim() != 2 or weight.dim() != 2 or targets.dim() != 1:
-            raise ValueError("hidden must be [tokens][H], weight [vocab][H] and targets [tokens]")
-        N, H = hidden.shape
-        V = weight.shape[0]
-        _check_on(hidden, self.device, (torch.bfloat16,), (N, H), "hidden")
-        _check_on(weight, self.device, (torch.bfloat16,), (V, H), "weight")
-        _check_on(targets, self.device, (torch.int64, torch.int32), (N,), "targets")
-        return N, V, H, targets.dtype == torch.int64
-
-    def vocab_loss(self, hidden, weight, targets, stream=None):
-        """Softmax cross entropy of hidden @ weight.T against targets without keeping the logits (dm0_vocab_loss).
-
-        hidden: bf16 [tokens][H]; weight: bf16 [vocab][H]; targets: int32 or int64 [tokens], negative: no target.
-        Returns (loss, lse), f32 [tokens]; -loss is the target's log probability, lse is for vocab_loss_grad."""
-        import torch
-        N, V, H, wide = self._vocab(hidden, weight, targets)
-        out = torch.empty((2, N), device=hidden.device, dtype=torch.float32)
-        loss, lse = out[0], out[1]
-        ws = self._workspace(self.lib.dm0_vocab_loss_workspace(N, V, H), stream)
-        self._chk(self.lib.dm0_vocab_loss(self.h, _ptr(hidden), _ptr(weight), _ptr(targets), wide, N, V, H, _ptr(loss),
-                                          _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
-        return loss, lse
-
-    def vocab_loss_grad(self, hidden, weight, targets, lse, dloss, dhidden=None, dweight=None,
-                        accumulate: bool = False, stream=None):
-        """Gradients of sum(dloss * loss) of vocab_loss with respect to hidden and weight (dm0_vocab_loss_grad).
-
-        lse, dloss: f32 [tokens].  dhidden [tokens][H] and dweight [vocab][H] are bf16 unless an fp32 tensor is
-        given; False leaves that gradient out.  accumulate adds to an fp32 dweight.  Returns (dhidden, dweight)."""
-        import torch
-        N, V, H, wide = self._vocab(hidden, weight, targets)
-        _check_on(lse, self.device, (torch.float32,), (N,), "lse")
-        _check_on(dloss, self.device, (torch.float32,), (N,), "dloss")
-        if accumulate and not isinstance(dweight, torch.Tensor):
-            raise ValueError("accumulate needs dweight")
-        grads = []
-        for t, like, name in ((dhidden, hidden, "dhidden"), (dweight, weight, "dweight")):
-            if t is None:
-                t = torch.empty_like(like)
-            elif t is False:
-                t = None
-            if t is not None:
-                _check_on(t, self.device, (torch.bfloat16, torch.float32), like.shape, name)
-            grads.append(t)
-        dh, dw = grads
-        ws = self._workspace(self.lib.dm0_vocab_loss_grad_workspace(N, V, H), stream)
-        self._chk(self.lib.dm0_vocab_loss_grad(
-            self.h, _ptr(hidden), _ptr(weight), _ptr(targets), wide, _ptr(lse), _ptr(dloss), N, V, H, _ptr(dh),
-            dh is not None and dh.dtype == torch.float32, _ptr(dw), dw is not None and dw.dtype == torch.float32,
-            accumulate, _ptr(ws), ws.numel(), _stream(stream)))
-        return dh, dw
 
     def debug_view(self, name: str) -> int:
         """Device address of an internal activation buffer (see dm0_debug_view)."""

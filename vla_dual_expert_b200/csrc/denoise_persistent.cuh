@@ -220,13 +220,6 @@ __device__ __forceinline__ void tma_load_3d_plain(void* dst, const CUtensorMap* 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// contiguous copy; both addresses 16-byte aligned, bytes a multiple of 16
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void pd_stage_wait(uint64_t* sbar, uint32_t par, volatile int* abort_flag) {
   if (!mbar_wait(sbar, par, abort_flag)) *abort_flag = 1;
 }

@@ -107,22 +107,32 @@ __global__ void __launch_bounds__(256) embed_kernel(const __nv_bfloat16* table, 
 }
 
 // ---------------------------------------------------------------- gradient: positions sorted by id
-constexpr int kEmbTile = 64;        // sorted positions per tile of the sums
+constexpr int kEmbTile = 64;        // sorted positions per tile of the sums; a longer segment is cut at tiles
 constexpr int kSortWarps = 32;
 constexpr int kSortMaxRows = 1600;  // vocabulary rows of one sorting CTA: 32 warps x 1600 counters = 200 KB
 
-// Each CTA owns `rows` consecutive vocabulary rows and reads every id: it counts the ids below its range
-// (its place in the sorted list, so the CTAs need no exchange), counts its own ids per (warp, row) with
-// warp w taking the w-th stretch of positions, and writes the positions in (row, position) order.  Ids are
-// read from L2 by every CTA: 148 x n x 8 bytes, 2 x 39 MB at 32768 tokens.
-//   perm[i], row_of[i]: position and id of sorted place i;  start[v]: first place of row v;
-//   start[vocab]: number of positions with a token.
-__global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, int n, int vocab, int rows, int* perm,
-                                                                     int* row_of, int* start, int* err) {
-  extern __shared__ int cnt[];   // [kSortWarps][rows], then the scan's warp totals
+// Scratch of one gradient.  Sorted place i holds position perm[i] of id row_of[i]; seg[v] is the range of
+// places of id v; total[0] the number of places; long_row[t] the id whose segment of more than kEmbTile
+// places begins in tile t, or -1 (there is at most one: it reaches behind the tile).
+struct EmbScratch {
+  int *perm, *row_of, *total, *long_row;
+  int2* seg;
+  float* part;   // [tile][2][H]: the tile's sums of a cut segment that began before it, and of one that begins in it
+};
+
+// Each of G CTAs (a power of two) owns the ids v with v mod G = its index, so that neighbouring frequent ids
+// fall to different CTAs.  Each reads every id: it counts those of smaller owners (its place in the sorted list,
+// so the CTAs need no exchange) and its own per (warp, row), warp w taking the w-th stretch of positions;
+// after a scan it writes the positions in (row, position) order.  The ids come from L2: G x n x 8 bytes,
+// twice.  A lane's rank among equal ids of its 32 is counted over the lanes that hold ids of this CTA, few
+// as a rule; match.any took 50 us here for the CTA of the most frequent ids, this 12 us (32768 tokens).
+__global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, int n, int vocab, int log_g, int rows,
+                                                                     EmbScratch o, int* err) {
+  extern __shared__ int cnt[];   // [kSortWarps][rows]
   __shared__ int warp_tot[kSortWarps], below_tot[kSortWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int v0 = blockIdx.x * rows, nb = min(rows, vocab - v0);
+  const int own = blockIdx.x, mask = (1 << log_g) - 1;
+  const int nb = (vocab - own + mask) >> log_g;   // ids own, own + G, ... below vocab
   for (int i = tid; i < kSortWarps * rows; i += blockDim.x) cnt[i] = 0;
   pdl_wait();
   __syncthreads();
@@ -142,20 +152,14 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       bad |= id[u] >= vocab;
-      below += id[u] >= 0 && id[u] < v0;
-      const unsigned bin = static_cast<unsigned>(id[u] - v0);
-      const bool in = id[u] >= 0 && bin < static_cast<unsigned>(nb);
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const unsigned peers = __match_any_sync(act, bin);
-        if (lane == __ffs(peers) - 1) mine[bin] += __popc(peers);
-      }
-      __syncwarp();
+      if (id[u] < 0 || id[u] >= vocab) continue;
+      below += (id[u] & mask) < own;
+      if ((id[u] & mask) == own) atomicAdd(&mine[id[u] >> log_g], 1);
     }
   }
   if (bad && blockIdx.x == 0) raise_error(err, kErrBounds);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+  for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
   if (lane == 0) below_tot[warp] = below;
   __syncthreads();
   int base = 0;
@@ -169,9 +173,9 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
       for (int w = 0; w < kSortWarps; ++w) tot += cnt[w * rows + r];
     int inc = tot;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
     }
     if (lane == 31) warp_tot[warp] = inc;
     __syncthreads();
@@ -182,17 +186,19 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
     }
     if (r < nb) {
       int at = carry + pre + inc - tot;
-      start[v0 + r] = at;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int k = cnt[w * rows + r];
-        cnt[w * rows + r] = at;
-        at += k;
-      }
+      o.seg[(static_cast<int64_t>(r) << log_g) + own] = make_int2(at, at + tot);
+      if (tot)
+        for (int w = 0; w < kSortWarps; ++w) {
+          const int k = cnt[w * rows + r];
+          cnt[w * rows + r] = at;
+          at += k;
+        }
     }
     carry += all;
     __syncthreads();
   }
-  if (tid == 0 && v0 + nb == vocab) start[vocab] = carry;
+  if (tid == 0 && own == mask) o.total[0] = carry;
+  if (carry == base) return;   // none of its ids occurs
   for (int b = p0; b < p1; b += 32 * U) {
     int id[U];
 #pragma unroll
@@ -202,70 +208,85 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const unsigned bin = static_cast<unsigned>(id[u] - v0);
-      const bool in = id[u] >= 0 && bin < static_cast<unsigned>(nb);
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const unsigned peers = __match_any_sync(act, bin);
-        const int lead = __ffs(peers) - 1;
-        int at = 0;
-        if (lane == lead) {
-          at = mine[bin];
-          mine[bin] = at + __popc(peers);
-        }
-        at = __shfl_sync(peers, at, lead) + __popc(peers & ((1u << lane) - 1u));
-        perm[at] = b + 32 * u + lane;
-        row_of[at] = id[u];
+      const bool in = id[u] >= 0 && id[u] < vocab && (id[u] & mask) == own;
+      unsigned act = __ballot_sync(0xffffffffu, in);
+      if (!act) continue;
+      int rank = 0, same = 0;
+      for (unsigned rest = act; rest; rest &= rest - 1) {
+        const int l = __ffs(rest) - 1;
+        const bool eq = __shfl_sync(0xffffffffu, id[u], l) == id[u];
+        same += eq;
+        rank += eq && l < lane;
       }
+      if (in) {
+        const int at = mine[id[u] >> log_g] + rank;
+        o.perm[at] = b + 32 * u + lane;
+        o.row_of[at] = id[u];
+      }
+      __syncwarp();
+      if (in && rank == 0) mine[id[u] >> log_g] += same;
       __syncwarp();
     }
   }
 }
 
-// Sums of the sorted rows.  Blocks [0, tiles * slices): one tile of sorted positions x 2048 columns, a
-// thread owning 8 columns and walking the tile's rows, eight requested ahead.  The remaining blocks write
-// the zero rows of ids that never occur (only when the gradient is written, not added to).
-//   part[tile][0]: the tile's sum of a segment that began before it; part[tile][1]: of one that goes on
-//   behind it.
+// Sums of the sorted rows.  Blocks [0, tiles * slices): one tile x 2048 columns, a thread owning 8 columns and
+// walking the tile's rows, eight requested ahead.  A segment of up to kEmbTile places belongs whole to the tile
+// where it begins (at most 127 rows a tile); a longer one is cut at the tiles and leaves partial sums.  The
+// remaining blocks write the zero rows of ids that never occur (only when the gradient is written, not added to).
 constexpr int kEmbCols = 2048;   // columns of one block: 256 threads x 8
 constexpr int kEmbZeroRows = 16;
 template <typename Td>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const int* perm, const int* row_of, const int* start,
-                                                        const Td* dout, RowsView dv, int n, int vocab, int H,
-                                                        float scale, float* grad, int accumulate, float* part,
-                                                        int tiles, int slices) {
+__global__ void __launch_bounds__(256) embed_sum_kernel(EmbScratch o, const Td* dout, RowsView dv, int vocab, int H,
+                                                        float scale, float* grad, int accumulate, int tiles,
+                                                        int slices) {
+  pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
   if (static_cast<int>(blockIdx.x) >= tiles * slices) {
     const int v0 = (blockIdx.x - tiles * slices) * kEmbZeroRows;
-    for (int v = v0; v < min(vocab, v0 + kEmbZeroRows); ++v) {
-      if (start[v] != start[v + 1]) continue;
-      float4* dst = reinterpret_cast<float4*>(grad + static_cast<int64_t>(v) * H);
+    const int my = v0 + (tid & 31);
+    const bool none = (tid & 31) < kEmbZeroRows && my < vocab && o.seg[my].x == o.seg[my].y;
+    for (unsigned todo = __ballot_sync(0xffffffffu, none); todo; todo &= todo - 1) {
+      float4* dst = reinterpret_cast<float4*>(grad + static_cast<int64_t>(v0 + __ffs(todo) - 1) * H);
       for (int c = tid; c < H / 4; c += blockDim.x) __stcs(dst + c, make_float4(0.f, 0.f, 0.f, 0.f));
     }
     return;
   }
   const int tile = blockIdx.x / slices, slice = blockIdx.x - tile * slices;
-  const int m = start[vocab];
-  const int i0 = tile * kEmbTile, i1 = min(m, i0 + kEmbTile);
-  if (i0 >= i1) return;
-  __shared__ int64_t src[kEmbTile];
-  __shared__ int row[kEmbTile + 1], beg, end;
-  if (tid < kEmbTile) {
-    const int i = i0 + tid;
-    src[tid] = i < i1 ? dv.off(perm[i]) : 0;
-    row[tid] = i < i1 ? row_of[i] : -1;
-  }
+  const int m = o.total[0];
+  const int i0 = tile * kEmbTile;
+  __shared__ int64_t src[2 * kEmbTile];
+  __shared__ int row[2 * kEmbTile];
+  __shared__ int range[2], cut[2];   // places of this tile; whether its first / last segment is cut
   if (tid == 0) {
-    row[kEmbTile] = -1;
-    beg = start[row_of[i0]];          // where the tile's first segment begins
-    end = start[row_of[i1 - 1] + 1];  // where its last one ends
+    int a = i0, b = min(m, i0 + kEmbTile), first = 0, last = 0, lrow = -1;
+    if (a < b) {
+      const int2 g0 = o.seg[o.row_of[a]];
+      first = g0.y - g0.x > kEmbTile && g0.x < a;           // goes on from an earlier tile
+      if (!first && g0.x < a) a = g0.y;                     // whole in an earlier tile
+      const int v1 = o.row_of[b - 1];
+      const int2 g1 = o.seg[v1];
+      if (g1.y - g1.x > kEmbTile) {
+        if (g1.x >= i0) last = 1, lrow = v1;                // begins here, goes on behind
+      } else if (g1.x >= i0) {
+        b = g1.y;
+      }
+    }
+    range[0] = a, range[1] = b, cut[0] = first, cut[1] = last;
+    if (slice == 0) o.long_row[tile] = lrow;
+  }
+  __syncthreads();
+  const int b0 = range[0], cnt = range[1] - b0;
+  if (cnt <= 0) return;
+  if (tid < cnt) {
+    src[tid] = dv.off(o.perm[b0 + tid]);
+    row[tid] = o.row_of[b0 + tid];
   }
   __syncthreads();
   const int c = slice * kEmbCols + tid * 8;
   if (c >= H) return;
   float acc[8] = {};
-  const int cnt = i1 - i0;
   for (int j0 = 0; j0 < cnt; j0 += 8) {
     float f[8][8];
 #pragma unroll
@@ -278,20 +299,17 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const int* perm, const i
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] += f[u][k];
       if (j + 1 < cnt && row[j + 1] == row[j]) continue;
-      // the segment of row[j] ends in this tile, or the tile ends
-      const bool first = row[j] == row[0], last = j + 1 == cnt;
-      const bool opened = first && beg < i0, open = last && end > i0 + kEmbTile;
-      float* dst;
-      if (opened || open) {
-        dst = part + (static_cast<int64_t>(tile) * 2 + (opened ? 0 : 1)) * H + c;
-        store8(dst, acc);
+      // the sum of row[j] in this tile is complete
+      const bool head = cut[0] && row[j] == row[0], tail = cut[1] && j + 1 == cnt;
+      if (head || tail) {
+        store8(o.part + (static_cast<int64_t>(tile) * 2 + (head ? 0 : 1)) * H + c, acc);
       } else {
-        dst = grad + static_cast<int64_t>(row[j]) * H + c;
-        float o[8] = {};
-        if (accumulate) load8_rw(dst, o);
+        float* dst = grad + static_cast<int64_t>(row[j]) * H + c;
+        float d[8] = {};
+        if (accumulate) load8_rw(dst, d);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = accumulate ? o[k] + scale * acc[k] : scale * acc[k];
-        store8(dst, o);
+        for (int k = 0; k < 8; ++k) d[k] = accumulate ? d[k] + scale * acc[k] : scale * acc[k];
+        store8(dst, d);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] = 0.f;
@@ -299,48 +317,50 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const int* perm, const i
   }
 }
 
-// The segments that cross tiles: the block of the tile where one begins adds its partials in tile order.
-// Eight groups of 32 lanes take stretches of the tiles, then the groups' sums are added in order.
-constexpr int kFixCols = 128;   // columns of one block: 32 lanes x 4
-__global__ void __launch_bounds__(256) embed_join_kernel(const int* row_of, const int* start, int vocab, int H,
-                                                         float scale, float* grad, int accumulate, const float* part) {
+// The cut segments: for each that begins in one of the block's 32 tiles, its partials are added in tile order,
+// by four groups of 64 lanes that take stretches of the tiles, then the groups' sums in order.
+constexpr int kFixCols = 256;   // columns of one block: 64 lanes x 4
+constexpr int kFixTiles = 32;
+__global__ void __launch_bounds__(256) embed_join_kernel(EmbScratch o, int tiles, int H, float scale, float* grad,
+                                                         int accumulate) {
   pdl_wait();
-  const int tile = blockIdx.x;
-  const int m = start[vocab];
-  const int i1 = (tile + 1) * kEmbTile;
-  if (i1 >= m) return;   // the last tile: nothing goes on behind it
-  const int v = row_of[i1 - 1];
-  const int beg = start[v], end = start[v + 1];
-  if (beg < tile * kEmbTile || end <= i1) return;   // begins elsewhere, or ends here
-  const int t1 = (end - 1) / kEmbTile;              // last tile of the segment
-  const int cnt = t1 - tile + 1;                    // partials: [tile][1], then [tile + 1 .. t1][0]
-  const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = blockIdx.x * kFixTiles;
+  const int l = threadIdx.x & 31;
+  const int my = t0 + l < tiles ? o.long_row[t0 + l] : -1;
+  const int g = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c = blockIdx.y * kFixCols + lane * 4;
-  const int per = (cnt + 7) / 8, k0 = g * per, k1 = min(cnt, k0 + per);
-  __shared__ float4 sum[8][32];
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < H) {
+  __shared__ float4 sum[4][64];
+  for (unsigned todo = __ballot_sync(0xffffffffu, my >= 0); todo; todo &= todo - 1) {   // the same in every warp
+    const int at = __ffs(todo) - 1;
+    const int v = __shfl_sync(0xffffffffu, my, at), tile = t0 + at;
+    const int cnt = (o.seg[v].y - 1) / kEmbTile - tile + 1;   // partials [tile][1], [tile + 1 ...][0]
+    const int per = (cnt + 3) / 4, k0 = g * per, k1 = min(cnt, k0 + per);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < H) {
 #pragma unroll 8
-    for (int k = k0; k < k1; ++k) {
-      const int64_t slot = static_cast<int64_t>(tile + k) * 2 + (k == 0 ? 1 : 0);
-      const float4 p = *reinterpret_cast<const float4*>(part + slot * H + c);
-      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+      for (int k = k0; k < k1; ++k) {
+        const int64_t slot = static_cast<int64_t>(tile + k) * 2 + (k == 0 ? 1 : 0);
+        const float4 p = *reinterpret_cast<const float4*>(o.part + slot * H + c);
+        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+      }
     }
+    sum[g][lane] = s;
+    __syncthreads();
+    if (g == 0 && c < H) {
+      for (int k = 1; k < 4; ++k) {
+        const float4 p = sum[k][lane];
+        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+      }
+      float4* dst = reinterpret_cast<float4*>(grad + static_cast<int64_t>(v) * H + c);
+      float4 d = make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w);
+      if (accumulate) {
+        const float4 old = *dst;
+        d = make_float4(d.x + old.x, d.y + old.y, d.z + old.z, d.w + old.w);
+      }
+      *dst = d;
+    }
+    __syncthreads();
   }
-  sum[g][lane] = s;
-  __syncthreads();
-  if (g != 0 || c >= H) return;
-  for (int k = 1; k < 8; ++k) {
-    const float4 p = sum[k][lane];
-    s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-  }
-  float4* dst = reinterpret_cast<float4*>(grad + static_cast<int64_t>(v) * H + c);
-  float4 o = make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w);
-  if (accumulate) {
-    const float4 d = *dst;
-    o = make_float4(o.x + d.x, o.y + d.y, o.z + d.z, o.w + d.w);
-  }
-  *dst = o;
 }
 
 }  // namespace dm0

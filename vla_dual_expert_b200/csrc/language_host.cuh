@@ -36,20 +36,21 @@ dm0_status rows_ok(dm0_ctx* c, const void* p, int f32, int T, int H, int64_t bat
 }
 
 struct EmbGradPlan {
-  int rows, sort_ctas, tiles, slices, zero_ctas;
-  size_t perm, row_of, start, part, bytes;
+  int log_g, rows, tiles, slices, zero_ctas;
+  size_t row_of, seg, total, long_row, part, bytes;
 };
 EmbGradPlan emb_grad_plan(int n, int vocab, int H) {
   EmbGradPlan p{};
-  p.rows = std::min(dm0::kSortMaxRows, std::max(1, (vocab + kLangSms - 1) / kLangSms));
-  p.sort_ctas = (vocab + p.rows - 1) / p.rows;
+  for (p.log_g = 7; (vocab + (1 << p.log_g) - 1) >> p.log_g > dm0::kSortMaxRows; ++p.log_g) {}
+  p.rows = (vocab + (1 << p.log_g) - 1) >> p.log_g;
   p.tiles = (n + dm0::kEmbTile - 1) / dm0::kEmbTile;
   p.slices = (H + dm0::kEmbCols - 1) / dm0::kEmbCols;
   p.zero_ctas = (vocab + dm0::kEmbZeroRows - 1) / dm0::kEmbZeroRows;
-  p.perm = 0;
   p.row_of = align256(sizeof(int) * static_cast<size_t>(n));
-  p.start = 2 * p.row_of;
-  p.part = p.start + align256(sizeof(int) * (static_cast<size_t>(vocab) + 1));
+  p.seg = 2 * p.row_of;
+  p.total = p.seg + align256(sizeof(int2) * static_cast<size_t>(vocab));
+  p.long_row = p.total + 256;
+  p.part = p.long_row + align256(sizeof(int) * static_cast<size_t>(p.tiles));
   p.bytes = p.part + align256(sizeof(float) * 2 * p.tiles * static_cast<size_t>(H));
   return p;
 }
@@ -58,19 +59,21 @@ template <typename Td>
 dm0_status embed_grad_run(dm0_ctx* c, cudaStream_t s, dm0::Ids ids, int n, const dm0::RowsView& v, int vocab, int H,
                           float scale, const Td* dout, float* grad, int accumulate, uint8_t* ws) {
   const EmbGradPlan p = emb_grad_plan(n, vocab, H);
-  int* perm = reinterpret_cast<int*>(ws + p.perm);
-  int* row_of = reinterpret_cast<int*>(ws + p.row_of);
-  int* start = reinterpret_cast<int*>(ws + p.start);
-  float* part = reinterpret_cast<float*>(ws + p.part);
-  TRY(launch(c, s, dm0::embed_sort_kernel, dim3(p.sort_ctas), dim3(dm0::kSortWarps * 32),
-             sizeof(int) * dm0::kSortWarps * p.rows, ids, n, vocab, p.rows, perm, row_of, start, c->d_err));
+  dm0::EmbScratch o{};
+  o.perm = reinterpret_cast<int*>(ws);
+  o.row_of = reinterpret_cast<int*>(ws + p.row_of);
+  o.seg = reinterpret_cast<int2*>(ws + p.seg);
+  o.total = reinterpret_cast<int*>(ws + p.total);
+  o.long_row = reinterpret_cast<int*>(ws + p.long_row);
+  o.part = reinterpret_cast<float*>(ws + p.part);
+  TRY(launch(c, s, dm0::embed_sort_kernel, dim3(1 << p.log_g), dim3(dm0::kSortWarps * 32),
+             sizeof(int) * dm0::kSortWarps * p.rows, ids, n, vocab, p.log_g, p.rows, o, c->d_err));
   TRY(launch(c, s, dm0::embed_sum_kernel<Td>, dim3(p.tiles * p.slices + (accumulate ? 0 : p.zero_ctas)), dim3(256), 0,
-             static_cast<const int*>(perm), static_cast<const int*>(row_of), static_cast<const int*>(start), dout, v, n,
-             vocab, H, scale, grad, accumulate, part, p.tiles, p.slices));
-  if (p.tiles < 2) return DM0_OK;
-  return launch(c, s, dm0::embed_join_kernel, dim3(p.tiles - 1, (H + dm0::kFixCols - 1) / dm0::kFixCols), dim3(256), 0,
-                static_cast<const int*>(row_of), static_cast<const int*>(start), vocab, H, scale, grad, accumulate,
-                static_cast<const float*>(part));
+             o, dout, v, vocab, H, scale, grad, accumulate, p.tiles, p.slices));
+  if (p.tiles < 2) return DM0_OK;   // no segment is longer than a tile
+  return launch(c, s, dm0::embed_join_kernel,
+                dim3((p.tiles + dm0::kFixTiles - 1) / dm0::kFixTiles, (H + dm0::kFixCols - 1) / dm0::kFixCols),
+                dim3(256), 0, o, p.tiles, H, scale, grad, accumulate);
 }
 
 // ---------------------------------------------------------------- residual norms
@@ -109,43 +112,62 @@ template <typename Th, typename Ty>
 dm0_status norm_run(dm0_ctx* c, cudaStream_t s, const dm0::RnArgs& a, const Th* h, const Ty* y, Th* h_out, bf16* n_out,
                     float* r_post, float* r_pre) {
   auto go = [&](auto kernel, int warps) {
-    const int rows = 8 / warps;
-    return launch(c, s, kernel, dim3((a.rows + rows - 1) / rows), dim3(256), 0, h, y, a, h_out, n_out, r_post, r_pre);
+    const int rows = warps > 4 ? 1 : 4 / warps;
+    return launch(c, s, kernel, dim3((a.rows + rows - 1) / rows), dim3(32 * warps * rows), 0, h, y, a, h_out, n_out,
+                  r_post, r_pre);
   };
-  if (a.H <= 256) return go(dm0::residual_norm_kernel<Th, Ty, 1, 1>, 1);
-  if (a.H <= 512) return go(dm0::residual_norm_kernel<Th, Ty, 2, 1>, 1);
-  if (a.H <= 1024) return go(dm0::residual_norm_kernel<Th, Ty, 4, 1>, 1);
-  if (a.H <= 2048) return go(dm0::residual_norm_kernel<Th, Ty, 8, 1>, 1);
-  if (a.H <= 4096) return go(dm0::residual_norm_kernel<Th, Ty, 8, 2>, 2);
-  return go(dm0::residual_norm_kernel<Th, Ty, 8, 4>, 4);
+  if (a.H <= 512) return go(dm0::residual_norm_kernel<Th, Ty, 1>, 1);
+  if (a.H <= 1024) return go(dm0::residual_norm_kernel<Th, Ty, 2>, 2);
+  if (a.H <= 2048) return go(dm0::residual_norm_kernel<Th, Ty, 4>, 4);
+  if (a.H <= 4096) return go(dm0::residual_norm_kernel<Th, Ty, 8>, 8);
+  return go(dm0::residual_norm_kernel<Th, Ty, 16>, 16);
 }
 
-// Stripes per sample of the backward pass: about four blocks per SM in all, at least one row each.
-int norm_stripes(int samples, int rows_per_sample) {
-  const int want = std::max(1, 4 * kLangSms / samples);
-  return std::min(want, rows_per_sample);
+int norm_grad_threads(int H) { return (H / 8 + 31) / 32 * 32; }
+// Stripes per sample of the backward pass: the blocks that are resident at once (512 threads per SM), at
+// least one row each; `per` rows a stripe.
+int norm_stripes(int samples, int rows_per_sample, int H, int* per) {
+  const int resident = kLangSms * std::max(1, std::min(8, 512 / norm_grad_threads(H)));
+  const int want = std::min(rows_per_sample, std::max(1, resident / samples));
+  *per = (rows_per_sample + want - 1) / want;
+  return (rows_per_sample + *per - 1) / *per;
 }
 int norm_samples(const dm0_norm* a) {
   return (a->gate && a->gate_stride) || ((a->mod_scale || a->mod_shift) && a->mod_stride) ? a->batch : 1;
 }
 size_t norm_grad_bytes(const dm0_norm* a) {
   const int samples = norm_samples(a), T = samples == 1 ? a->batch * a->tokens : a->tokens;
-  return align256(sizeof(float) * 3 * a->hidden * static_cast<size_t>(samples) * norm_stripes(samples, T));
+  int per = 0;
+  return align256(sizeof(float) * 3 * a->hidden * static_cast<size_t>(samples) * norm_stripes(samples, T, a->hidden, &per));
 }
 
 template <typename Tn, typename Th, typename Ty>
-dm0_status norm_grad_run(dm0_ctx* c, cudaStream_t s, const dm0::RnGradArgs& a, int samples, const Tn* dn,
+dm0_status norm_grad_run(dm0_ctx* c, cudaStream_t s, dm0::RnGradArgs a, int samples, const Tn* dn,
                          const Th* dh_out, const Th* h_out, const Ty* y, Th* dh, Ty* dy) {
-  const int threads = (a.f.H / 8 + 31) / 32 * 32;
+  const int threads = norm_grad_threads(a.f.H);
+  const size_t row = static_cast<size_t>(a.f.H) * (sizeof(Tn) + (dh_out ? 2 : 1) * sizeof(Th) + (y ? sizeof(Ty) : 0));
+  // rows in the ring: four, or as many as leave room for the other resident blocks (at most 128 KB a row)
+  const size_t room = threads <= 256 ? size_t(200) * 1024 / std::min(8, 512 / threads) : size_t(200) * 1024;
+  a.stages = static_cast<int>(std::max<size_t>(1, std::min<size_t>(dm0::kRnMaxStages, room / row)));
   auto go = [&](auto kernel) {
-    return launch(c, s, kernel, dim3(samples * a.stripes), dim3(threads), 0, dn, dh_out, h_out, y, a, dh, dy);
+    return launch(c, s, kernel, dim3(samples * a.stripes), dim3(threads), a.stages * row, dn, dh_out, h_out, y, a, dh, dy);
   };
   if (threads <= 256) return go(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 256>);
+  if (threads <= 512) return go(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 512>);
   return go(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 1024>);
 }
 
+template <typename Tn, typename Th, typename Ty>
+bool norm_grad_setup() {
+  auto attr = [&](auto kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  return attr(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 256>, 128 * 1024) &&
+         attr(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 512>, 200 * 1024) &&
+         attr(dm0::residual_norm_grad_kernel<Tn, Th, Ty, 1024>, 200 * 1024);
+}
+
 // ---------------------------------------------------------------- vocabulary loss
-constexpr int kVgStages = 4;
 constexpr int kVgPieceElems = 1 << 27;   // entries of G held at a time: 256 MB of workspace
 
 // bf16 [rows][cols] map of 64-column boxes of `box` rows, 128-byte swizzle (nothing is kept by address)
@@ -160,15 +182,19 @@ dm0_status vg_tmap(dm0_ctx* c, CUtensorMap* m, const void* p, uint64_t rows, uin
   return r == CUDA_SUCCESS ? DM0_OK : fail(c, DM0_ECUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
 }
 
+// More than 128 tokens: pairs of CTAs on 256 x 256 tiles; up to 128: one CTA on 128 x 256, where a pair's
+// second half of the rows would be padding.
+bool vocab_pairs(int tokens) { return tokens > 128; }
+int vocab_tile_rows(int tokens) { return vocab_pairs(tokens) ? 256 : 128; }
+
 struct VocabLossPlan {
-  int bn, mt, nt, part_ld;
+  int mt, nt, part_ld;
   size_t part, zt, bytes;
 };
 VocabLossPlan vocab_loss_plan(int tokens, int vocab) {
   VocabLossPlan p{};
-  p.mt = (tokens + 127) / 128;
-  p.bn = 256;
-  p.nt = (vocab + p.bn - 1) / p.bn;
+  p.mt = (tokens + vocab_tile_rows(tokens) - 1) / vocab_tile_rows(tokens);
+  p.nt = (vocab + 255) / 256;
   p.part_ld = (tokens + 31) / 32 * 32;
   p.part = 0;
   p.zt = align256(sizeof(float2) * 2 * p.nt * static_cast<size_t>(p.part_ld));
@@ -187,13 +213,14 @@ VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
   const int pieces = (vr + most - 1) / most;
   p.piece = ((vr + pieces - 1) / pieces + 255) / 256 * 256;
   // splits of dh's contraction over the piece: whole waves of tiles against the traffic of the fp32 sums
-  const int64_t tiles = static_cast<int64_t>((tokens + 127) / 128) * ((H + 255) / 256);
+  const int rows = vocab_tile_rows(tokens), workers = vocab_pairs(tokens) ? kLangSms / 2 : kLangSms;
+  const int64_t tiles = static_cast<int64_t>((tokens + rows - 1) / rows) * ((H + 255) / 256);
   const int KB = (std::min(p.piece, vocab) + 63) / 64;   // of the first piece, whose splits all write
   double best = 0;
   for (int S = 1; S <= std::min(KB, 64); ++S) {
     const int per = (KB + S - 1) / S, used = (KB + per - 1) / per;
     if (used != S) continue;
-    const double t = static_cast<double>((tiles * S + kLangSms - 1) / kLangSms) * (per * 0.28 + 1.0) +
+    const double t = static_cast<double>((tiles * S + workers - 1) / workers) * (per * 0.28 + 1.0) +
                      S * 8.0 * tokens * H / 6.0e6;
     if (S == 1 || t < best) best = t, p.splits = S, p.kb_per_split = per;
   }
@@ -213,21 +240,26 @@ dm0_status vocab_ok(dm0_ctx* c, const void* h, const void* w, const void* t, int
   return DM0_OK;
 }
 
-template <int MODE, int BN>
-dm0_status vocab_gemm(dm0_ctx* c, cudaStream_t s, const CUtensorMap& ta, const CUtensorMap& tb, dm0::VgArgs a) {
+template <int MODE>
+dm0_status vocab_gemm(dm0_ctx* c, cudaStream_t s, bool pairs, const CUtensorMap& ta, const CUtensorMap& tb,
+                      const dm0::VgArgs& a) {
   const int64_t tiles = static_cast<int64_t>(a.mt) * a.nt * a.splits;
   if (tiles > 0x3fffffff) return fail(c, DM0_ESHAPE, "too many tiles");
-  return launch(c, s, dm0::vocab_gemm_kernel<MODE, BN, kVgStages>,
-                dim3(static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms))), dim3(320),
-                dm0::VgSmem<BN, kVgStages>::kBytes, ta, tb, a);
+  if (pairs)
+    return launch(c, s, dm0::vocab_gemm_pair_kernel<MODE>,
+                  dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms / 2))), dim3(320),
+                  dm0::VgTile<true>::kBytes, ta, tb, a);
+  return launch(c, s, dm0::vocab_gemm_kernel<MODE>, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms))),
+                dim3(320), dm0::VgTile<false>::kBytes, ta, tb, a);
 }
 
 dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16* w, dm0::Ids tgt, int tokens, int vocab,
                           int H, float* loss, float* lse, uint8_t* ws) {
   const VocabLossPlan p = vocab_loss_plan(tokens, vocab);
   CUtensorMap ta, tb;
+  const bool pairs = vocab_pairs(tokens);
   TRY(vg_tmap(c, &ta, h, tokens, H, 128));
-  TRY(vg_tmap(c, &tb, w, vocab, H, p.bn));
+  TRY(vg_tmap(c, &tb, w, vocab, H, pairs ? 128 : 256));
   dm0::VgArgs a{};
   a.M = tokens;
   a.N = vocab;
@@ -243,8 +275,8 @@ dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.part_ld = p.part_ld;
   a.zt = reinterpret_cast<float*>(ws + p.zt);
-  TRY((vocab_gemm<dm0::kVgStats, 256>(c, s, ta, tb, a)));
-  return launch(c, s, dm0::vocab_loss_kernel, dim3((tokens + 31) / 32), dim3(512), 0,
+  TRY(vocab_gemm<dm0::kVgStats>(c, s, pairs, ta, tb, a));
+  return launch(c, s, dm0::vocab_loss_kernel, dim3((tokens + 3) / 4), dim3(512), 0,
                 static_cast<const float2*>(a.part), 2 * p.nt, p.part_ld, static_cast<const float*>(a.zt), tgt, tokens,
                 vocab, loss, lse, c->d_err);
 }
@@ -257,14 +289,16 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   bf16* g = reinterpret_cast<bf16*>(ws + p.g);
   float* part = reinterpret_cast<float*>(ws + p.dh);
   TRY(launch(c, s, dm0::vocab_scale_kernel, dim3(1), dim3(1024), 0, dloss, tgt, tokens, vocab, scale, c->d_err));
+  const bool pairs = vocab_pairs(tokens);
+  const int tr = vocab_tile_rows(tokens);
   CUtensorMap h_k, w_k, g_k, w_mn, g_mn, h_mn;
   TRY(vg_tmap(c, &h_k, h, tokens, H, 128));
-  TRY(vg_tmap(c, &w_k, w, vocab, H, 256));
+  TRY(vg_tmap(c, &w_k, w, vocab, H, pairs ? 128 : 256));
   TRY(vg_tmap(c, &g_k, g, tokens, p.piece, 128));
   TRY(vg_tmap(c, &w_mn, w, vocab, H, 64));
   TRY(vg_tmap(c, &g_mn, g, tokens, p.piece, 64));
   TRY(vg_tmap(c, &h_mn, h, tokens, H, 64));
-  const int mt = (tokens + 127) / 128, ht = (H + 255) / 256;
+  const int mt = (tokens + tr - 1) / tr, ht = (H + 255) / 256;
   for (int v0 = 0; v0 < vocab; v0 += p.piece) {
     const int cols = std::min(p.piece, vocab - v0);
     dm0::VgArgs a{};
@@ -287,7 +321,7 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
     a.dloss = dloss;
     a.g = g;
     a.ldg = p.piece;
-    TRY((vocab_gemm<dm0::kVgGrad, 256>(c, s, h_k, w_k, a)));
+    TRY(vocab_gemm<dm0::kVgGrad>(c, s, pairs, h_k, w_k, a));
     if (dh) {
       a.N = H;
       a.K = cols;
@@ -297,13 +331,13 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
       a.band = 1;
       a.dh = part;
       a.add = v0 > 0;
-      TRY((vocab_gemm<dm0::kVgHidden, 256>(c, s, g_k, w_mn, a)));
+      TRY(vocab_gemm<dm0::kVgHidden>(c, s, pairs, g_k, w_mn, a));
     }
     if (dw) {
       a.M = cols;
       a.N = H;
       a.K = tokens;
-      a.mt = (cols + 127) / 128;
+      a.mt = (cols + tr - 1) / tr;
       a.nt = ht;
       a.splits = 1;
       a.kb_per_split = (tokens + 63) / 64;
@@ -312,7 +346,7 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
       a.add = accumulate;
       a.dw = dw;
       a.dw_f32 = dw_f32;
-      TRY((vocab_gemm<dm0::kVgWeight, 256>(c, s, g_mn, h_mn, a)));
+      TRY(vocab_gemm<dm0::kVgWeight>(c, s, pairs, g_mn, h_mn, a));
     }
   }
   if (!dh) return DM0_OK;
@@ -327,17 +361,26 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
                 static_cast<const float*>(scale), static_cast<bf16*>(dh));
 }
 
+template <int MODE>
+bool vocab_setup() {
+  return cudaFuncSetAttribute(dm0::vocab_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              dm0::VgTile<false>::kBytes) == cudaSuccess &&
+         cudaFuncSetAttribute(dm0::vocab_gemm_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              dm0::VgTile<true>::kBytes) == cudaSuccess;
+}
+
 // shared-memory limits of these kernels (dm0_create)
 bool lang_setup() {
   auto attr = [](auto kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  const int v = dm0::VgSmem<256, kVgStages>::kBytes;
-  return attr(dm0::embed_sort_kernel, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
-         attr(dm0::vocab_gemm_kernel<dm0::kVgStats, 256, kVgStages>, v) &&
-         attr(dm0::vocab_gemm_kernel<dm0::kVgGrad, 256, kVgStages>, v) &&
-         attr(dm0::vocab_gemm_kernel<dm0::kVgHidden, 256, kVgStages>, v) &&
-         attr(dm0::vocab_gemm_kernel<dm0::kVgWeight, 256, kVgStages>, v);
+  typedef float f;
+  return norm_grad_setup<f, f, f>() && norm_grad_setup<f, f, bf16>() && norm_grad_setup<f, bf16, f>() &&
+         norm_grad_setup<f, bf16, bf16>() && norm_grad_setup<bf16, f, f>() && norm_grad_setup<bf16, f, bf16>() &&
+         norm_grad_setup<bf16, bf16, f>() && norm_grad_setup<bf16, bf16, bf16>() &&
+         attr(dm0::embed_sort_kernel, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
+         vocab_setup<dm0::kVgStats>() && vocab_setup<dm0::kVgGrad>() && vocab_setup<dm0::kVgHidden>() &&
+         vocab_setup<dm0::kVgWeight>();
 }
 }  // namespace
 
@@ -442,7 +485,8 @@ dm0_status dm0_residual_norm_grad(dm0_ctx* c, const dm0_norm* a, const void* dn,
   r.f = norm_args(c, a);
   r.r_post = r_post;
   r.r_pre = r_pre;
-  r.stripes = norm_stripes(samples, r.f.rows_per_sample);
+  r.stripes = norm_stripes(samples, r.f.rows_per_sample, a->hidden, &r.per);
+  r.err = c->d_err;
   r.part = sums ? static_cast<float*>(workspace) : nullptr;
   TRY(DM0_BY_TYPE(dn_f32, Tn, {
     return DM0_BY_TYPE(a->h_f32, Th, {

@@ -48,9 +48,14 @@ struct VgArgs {
   int dw_f32;
 };
 
-template <int BN, int STAGES>
-struct VgSmem {
-  static constexpr uint32_t kA = 128 * 128, kB = BN * 128, kStage = kA + kB, kPipe = STAGES * kStage;
+// Tile of a CTA, or of a CTA pair (cta_group::2): 128 or 256 rows of A times 256 rows of B.  A pair's CTAs
+// each stage half of A's and of B's rows, so a k-block takes 32 KB of each CTA's shared memory instead of 48.
+template <bool PAIR>
+struct VgTile {
+  static constexpr int kM = PAIR ? 256 : 128, kN = 256;
+  static constexpr int kBRows = PAIR ? 128 : 256;   // of B, per CTA
+  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr uint32_t kA = 128 * 128, kB = kBRows * 128, kStage = kA + kB, kPipe = kStages * kStage;
   static constexpr uint32_t kScr = kPipe;                 // 8 x 4 KB
   static constexpr uint32_t kBar = kScr + 8 * 4096;
   static constexpr uint32_t kBytes = kBar + 256 + 1024;   // barriers, alignment slack
@@ -108,45 +113,60 @@ __device__ __forceinline__ void vg_store_f32(uint8_t* scr, const float (&v)[32],
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Warp 0: TMA; warp 1: TMEM and MMA; warps 2..9: epilogue, two per TMEM lane quarter (column halves).
-// Persistent: one CTA per SM walks the tiles; the accumulator is double-buffered.
-template <int MODE, int BN, int STAGES>
-__global__ void __launch_bounds__(320, 1)
-    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const VgArgs a) {
-  using L = VgSmem<BN, STAGES>;
+// The tensor cores' fp32 accumulator drops the bits below its last place instead of rounding them, so a long
+// sum loses up to that at each of its K / 16 steps, always toward zero.  The logits behind the loss are
+// therefore added in stretches of kVgStretch k-blocks (512 of K), each from zero, and the stretches in fp32
+// registers; the gradient's operand is rounded to bf16 and needs none of it.
+constexpr int kVgStretch = 8;
+
+// Warp 0: TMA; warp 1: TMEM and, in a pair's first CTA, MMA; warps 2..9: epilogue, two per TMEM lane quarter
+// (column halves).  Persistent: one CTA per SM, or one pair per two, walks the tiles; the accumulator is
+// double-buffered.  In a pair the copies of both CTAs count on the first one's `full`, its MMAs free both
+// CTAs' stages and fill both accumulators, and both epilogues free its `tempty`.
+template <int MODE, bool PAIR>
+__device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const VgArgs& a) {
+  using L = VgTile<PAIR>;
+  constexpr int kStages = L::kStages, kN = L::kN;
   constexpr bool kAMn = MODE == kVgWeight, kBMn = MODE == kVgHidden || MODE == kVgWeight;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
+  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
   const int KB = (a.K + 63) >> 6;
   const int plane = a.mt * a.nt, ntiles = plane * a.splits;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 8);
+      mbar_init(&tempty[i], PAIR ? 16 : 8);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 2 * BN);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, 2 * kN);
+    } else {
+      tmem_alloc(tmem_slot, 2 * kN);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();   // the other CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
@@ -158,6 +178,7 @@ __global__ void __launch_bounds__(320, 1)
     kb0 = split * a.kb_per_split;
     kb1 = min(KB, kb0 + a.kb_per_split);
   };
+  auto stretch_end = [&](int kb, int kb1) { return MODE == kVgStats ? min(kb1, kb + kVgStretch) : kb1; };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -165,211 +186,291 @@ __global__ void __launch_bounds__(320, 1)
       tma_prefetch_desc(&tmB);
       const uint64_t keep = policy_evict_last();
       int it = 0;
-      for (int t = blockIdx.x; t < ntiles && !*abort_flag; t += gridDim.x) {
+      for (int t = worker; t < ntiles && !*abort_flag; t += workers) {
         int m, n, kb0, kb1, split;
         tile_at(t, m, n, kb0, kb1, split);
+        const int ra = m * L::kM + rank * 128, rb = n * kN + rank * L::kBRows;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (it >= STAGES && !mbar_wait(&empty[s], ((it / STAGES) - 1) & 1, abort_flag)) {
+          const int s = it % kStages;
+          if (it >= kStages && !mbar_wait(&empty[s], ((it / kStages) - 1) & 1, abort_flag)) {
             *abort_flag = 1;
             raise_error(a.err, kErrTimeoutProducer);
             break;
           }
           uint8_t* sa = smem + s * L::kStage;
           uint8_t* sb = sa + L::kA;
-          mbar_arrive_expect_tx(&full[s], L::kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], PAIR ? 2 * L::kStage : L::kStage);
+          const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
+          auto load = [&](uint8_t* dst, const CUtensorMap& map, int x, int y) {
+            if constexpr (PAIR)
+              tma_load_2d_pair(dst, &map, bar, x, y, keep);
+            else
+              tma_load_2d(dst, &map, &full[s], x, y, keep);
+          };
           if constexpr (kAMn) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) tma_load_2d(sa + 8192 * j, &tmA, &full[s], m * 128 + 64 * j, kb * 64, keep);
+            for (int j = 0; j < 2; ++j) load(sa + 8192 * j, tmA, ra + 64 * j, kb * 64);
           } else {
-            tma_load_2d(sa, &tmA, &full[s], kb * 64, m * 128, keep);
+            load(sa, tmA, kb * 64, ra);
           }
           if constexpr (kBMn) {
 #pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(sb + 8192 * j, &tmB, &full[s], n * BN + 64 * j, a.b_y0 + kb * 64, keep);
+            for (int j = 0; j < L::kBRows / 64; ++j) load(sb + 8192 * j, tmB, rb + 64 * j, a.b_y0 + kb * 64);
           } else {
-            tma_load_2d(sb, &tmB, &full[s], kb * 64, a.b_y0 + n * BN, keep);
+            load(sb, tmB, kb * 64, a.b_y0 + rb);
           }
         }
       }
-      for (int i = it - STAGES; i < it; ++i) {   // copies in flight land before the CTA exits
-        if (i < 0) continue;
-        if (!mbar_wait(&full[i % STAGES], (i / STAGES) & 1, nullptr, kDrainTimeoutNs)) raise_error(a.err, kErrDrain);
-      }
+      // copies in flight land before the CTA exits (a pair's, both CTAs': the first one waits for them, the
+      // other for it)
+      if (rank == 0)
+        for (int i = it - kStages; i < it; ++i) {
+          if (i < 0) continue;
+          if (!mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, kDrainTimeoutNs)) raise_error(a.err, kErrDrain);
+        }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, BN) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(L::kM, kN) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (PAIR)
+          umma_commit_pair(bar);
+        else
+          umma_commit(bar);
+      };
       int it = 0, local = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < ntiles; t += gridDim.x, ++local) {
+      for (int t = worker; ok && t < ntiles; t += workers) {
         int m, n, kb0, kb1, split;
         tile_at(t, m, n, kb0, kb1, split);
-        const int buf = local & 1;
-        if (local >= 2 && !mbar_wait(&tempty[buf], ((local >> 1) - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait(&full[s], (it / STAGES) & 1, abort_flag)) {
+        for (int ks = kb0; ok && ks < kb1; ++local) {
+          const int ke = stretch_end(ks, kb1), buf = local & 1;
+          const uint32_t freed = ((local >> 1) - 1) & 1;
+          if (local >= 2 && !(PAIR ? mbar_wait_cluster(&tempty[buf], freed, abort_flag)
+                                   : mbar_wait(&tempty[buf], freed, abort_flag))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t aa = smem_u32(smem + s * L::kStage), bb = aa + L::kA;
+          for (int kb = ks; kb < ke; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait(&full[s], (it / kStages) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t aa = smem_u32(smem + s * L::kStage), bb = aa + L::kA;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t da = kAMn ? sw128_mnmajor_desc(aa + 2048 * kk, 8192) : sw128_kmajor_desc(aa + 32 * kk);
-            const uint64_t db = kBMn ? sw128_mnmajor_desc(bb + 2048 * kk, 8192) : sw128_kmajor_desc(bb + 32 * kk);
-            umma_bf16(tmem + buf * BN, da, db, idesc, (kb > kb0 || kk != 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t da = kAMn ? sw128_mnmajor_desc(aa + 2048 * kk, 8192) : sw128_kmajor_desc(aa + 32 * kk);
+              const uint64_t db = kBMn ? sw128_mnmajor_desc(bb + 2048 * kk, 8192) : sw128_kmajor_desc(bb + 32 * kk);
+              const uint32_t acc = (kb > ks || kk != 0) ? 1u : 0u;
+              if constexpr (PAIR)
+                umma_bf16_pair(tmem + buf * kN, da, db, idesc, acc);
+              else
+                umma_bf16(tmem + buf * kN, da, db, idesc, acc);
+            }
+            commit(&empty[s]);
           }
-          umma_commit(&empty[s]);
+          if (ok) commit(&tfull[buf]);
+          ks = ke;
         }
-        if (ok) umma_commit(&tfull[buf]);
       }
       if (!ok) {
         *abort_flag = 1;
         raise_error(a.err, kErrTimeoutMma);
       }
-      umma_commit(drain);
+      commit(drain);
       if (!mbar_wait(drain, 0, nullptr, kWaitTimeoutNs + kDrainTimeoutNs)) raise_error(a.err, kErrDrain);
     }
   } else {
     const int lane_base = (warp & 3) * 32, half = (warp - 2) >> 2;
     uint8_t* scr = smem + L::kScr + (warp - 2) * 4096;
-    constexpr int kCols = BN / 2;   // columns of this warp
+    constexpr int kCols = kN / 2;   // columns of this warp
     const float s = MODE == kVgGrad || MODE == kVgWeight ? a.scale[0] : 1.f;
     int local = 0;
-    for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++local) {
-      int m, n, kb0, kb1, split;
-      tile_at(t, m, n, kb0, kb1, split);
-      const int buf = local & 1;
-      if (!mbar_wait(&tfull[buf], (local >> 1) & 1, abort_flag)) {
-        *abort_flag = 1;
-        raise_error(a.err, kErrTimeoutEpilogue);
-        break;
+    auto ready = [&]() {   // the next accumulator of this CTA is complete
+      if (mbar_wait(&tfull[local & 1], (local >> 1) & 1, abort_flag)) {
+        tc_fence_after();
+        return true;
       }
-      tc_fence_after();
-      const uint32_t tm = tmem + (static_cast<uint32_t>(lane_base) << 16) + buf * BN + half * kCols;
-      const int row0 = m * 128 + lane_base, row = row0 + lane;
-      const int col0 = n * BN + half * kCols;
-      const int rows = min(32, a.M - row0);   // rows of this warp to store (may be <= 0)
-      if constexpr (MODE == kVgStats) {
-        const int tgt = row < a.M ? a.targets.get(row) : -1;
-        float mx = -INFINITY, sum = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < kCols / 32; ++c) {
-          float v[32];
-          tmem_ld32(tm + 32 * c, v);
-          const int cc = col0 + 32 * c;
-          if (cc + 32 > a.valid_n) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (cc + j >= a.valid_n) v[j] = -INFINITY;
-          }
-          float cm = mx;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) cm = max3f(cm, v[j], v[j + 1]);
-          const float ref = cm == -INFINITY ? 0.f : cm * kLog2e;
-          float acc = sum * ex2_fast(mx * kLog2e - ref);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc += ex2_fast(fmaf(v[j], kLog2e, -ref));
-          sum = acc;
-          mx = cm;
-          const unsigned at = static_cast<unsigned>(tgt - cc);
-          if (tgt >= 0 && at < 32u && tgt < a.vocab) {
-            float z = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z = at == static_cast<unsigned>(j) ? v[j] : z;
-            a.zt[row] = z;
-          }
-        }
-        if (row < a.M) a.part[static_cast<int64_t>(2 * n + half) * a.part_ld + row] = make_float2(mx, sum);
-      } else if constexpr (MODE == kVgGrad) {
-        int tgt = -1;
-        float l2 = 0.f, gi = 0.f;
-        if (row < a.M) {
-          tgt = a.targets.get(row);
-          if (tgt >= a.vocab) tgt = -1;
-          l2 = a.lse[row] * kLog2e;
-          gi = a.dloss[row] / s;
-        }
-        const int rel = tgt - a.v0;   // column of the target in this piece (maybe outside)
-#pragma unroll 1
-        for (int c = 0; c < kCols / 64; ++c) {
-          float v[2][32];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tmem_ld32(tm + 64 * c + 32 * q, v[q]);
-            const int cc = col0 + 64 * c + 32 * q;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[q][j] = ex2_fast(fmaf(v[q][j], kLog2e, -l2)) * gi;
-            if (static_cast<unsigned>(rel - cc) < 32u) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (rel - cc == j) v[q][j] -= gi;
-            }
-            if (tgt < 0 || cc + 32 > a.valid_n) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (tgt < 0 || cc + j >= a.valid_n) v[q][j] = 0.f;
-            }
-          }
-          vg_store_bf16(scr, v[0], v[1], a.g + static_cast<int64_t>(row0) * a.ldg + col0 + 64 * c, a.ldg, rows);
-        }
-      } else if constexpr (MODE == kVgHidden) {
-        float* dst = a.dh + (static_cast<int64_t>(split) * a.M + row0) * a.N + col0;
-#pragma unroll 1
-        for (int c = 0; c < kCols / 32; ++c) {
-          float v[32];
-          tmem_ld32(tm + 32 * c, v);
-          if (col0 + 32 * c < a.N) vg_store_f32(scr, v, dst + 32 * c, a.N, rows, a.add != 0);
-        }
-      } else {
-        const int64_t at = static_cast<int64_t>(a.v0 + row0) * a.N + col0;
-#pragma unroll 1
-        for (int c = 0; c < kCols / 64; ++c) {
-          float v[2][32];
-          tmem_ld32(tm + 64 * c, v[0]);
-          tmem_ld32(tm + 64 * c + 32, v[1]);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[q][j] *= s;
-          if (col0 + 64 * c >= a.N) continue;
-          if (a.dw_f32) {
-            float* dst = static_cast<float*>(a.dw) + at + 64 * c;
-            vg_store_f32(scr, v[0], dst, a.N, rows, a.add != 0);
-            vg_store_f32(scr, v[1], dst + 32, a.N, rows, a.add != 0);
-          } else {
-            vg_store_bf16(scr, v[0], v[1], static_cast<__nv_bfloat16*>(a.dw) + at + 64 * c, a.N, rows);
-          }
-        }
-      }
+      *abort_flag = 1;
+      raise_error(a.err, kErrTimeoutEpilogue);
+      return false;
+    };
+    auto release = [&]() {   // and read
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[buf]);
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_cluster(cluster_addr(&tempty[local & 1], 0));
+        else
+          mbar_arrive(&tempty[local & 1]);
+      }
+      ++local;
+    };
+    const uint32_t tm0 = tmem + (static_cast<uint32_t>(lane_base) << 16) + half * kCols;
+    bool go = true;
+    for (int t = worker; go && t < ntiles; t += workers) {
+      int m, n, kb0, kb1, split;
+      tile_at(t, m, n, kb0, kb1, split);
+      const int row0 = m * L::kM + rank * 128 + lane_base, row = row0 + lane;
+      const int col0 = n * kN + half * kCols;
+      const int rows = min(32, a.M - row0);   // rows of this warp to store (may be <= 0)
+      if constexpr (MODE == kVgStats) {
+        float v[kCols / 32][32];
+        for (int ks = kb0; ks < kb1; ks = stretch_end(ks, kb1)) {
+          if (!ready()) {
+            go = false;
+            break;
+          }
+          const uint32_t tm = tm0 + (local & 1) * kN;
+          if (ks == kb0) {
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tm + 32 * c, v[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) {
+              float x[32];
+              tmem_ld32(tm + 32 * c, x);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[c][j] += x[j];
+            }
+          }
+          release();
+        }
+        if (!go) break;
+        const int tgt = row < a.M ? a.targets.get(row) : -1;
+        if (col0 + kCols > a.valid_n) {
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col0 + 32 * c + j >= a.valid_n) v[c][j] = -INFINITY;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) mx = max3f(mx, v[c][j], v[c][j + 1]);
+        if (static_cast<unsigned>(tgt - col0) < static_cast<unsigned>(kCols) && tgt < a.vocab) {
+          float z = 0.f;
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z = tgt - col0 == 32 * c + j ? v[c][j] : z;
+          a.zt[row] = z;
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx * kLog2e;
+        float sum[4] = {};
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[j & 3] += ex2_fast(fmaf(v[c][j], kLog2e, -ref));
+        if (row < a.M)
+          a.part[static_cast<int64_t>(2 * n + half) * a.part_ld + row] =
+              make_float2(mx, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+      } else {
+        if (!ready()) break;
+        const uint32_t tm = tm0 + (local & 1) * kN;
+        if constexpr (MODE == kVgGrad) {
+          int tgt = -1;
+          float l2 = 0.f, gi = 0.f;
+          if (row < a.M) {
+            tgt = a.targets.get(row);
+            if (tgt >= a.vocab) tgt = -1;
+            l2 = a.lse[row] * kLog2e;
+            gi = a.dloss[row] / s;
+          }
+          const int rel = tgt - a.v0;   // column of the target in this piece (maybe outside)
+#pragma unroll 1
+          for (int c = 0; c < kCols / 64; ++c) {
+            float v[2][32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              tmem_ld32(tm + 64 * c + 32 * q, v[q]);
+              const int cc = col0 + 64 * c + 32 * q;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[q][j] = ex2_fast(fmaf(v[q][j], kLog2e, -l2)) * gi;
+              if (static_cast<unsigned>(rel - cc) < 32u) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (rel - cc == j) v[q][j] -= gi;
+              }
+              if (tgt < 0 || cc + 32 > a.valid_n) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (tgt < 0 || cc + j >= a.valid_n) v[q][j] = 0.f;
+              }
+            }
+            vg_store_bf16(scr, v[0], v[1], a.g + static_cast<int64_t>(row0) * a.ldg + col0 + 64 * c, a.ldg, rows);
+          }
+        } else if constexpr (MODE == kVgHidden) {
+          float* dst = a.dh + (static_cast<int64_t>(split) * a.M + row0) * a.N + col0;
+#pragma unroll 1
+          for (int c = 0; c < kCols / 32; ++c) {
+            float v[32];
+            tmem_ld32(tm + 32 * c, v);
+            if (col0 + 32 * c < a.N) vg_store_f32(scr, v, dst + 32 * c, a.N, rows, a.add != 0);
+          }
+        } else {
+          const int64_t at = static_cast<int64_t>(a.v0 + row0) * a.N + col0;
+#pragma unroll 1
+          for (int c = 0; c < kCols / 64; ++c) {
+            float v[2][32];
+            tmem_ld32(tm + 64 * c, v[0]);
+            tmem_ld32(tm + 64 * c + 32, v[1]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[q][j] *= s;
+            if (col0 + 64 * c >= a.N) continue;
+            if (a.dw_f32) {
+              float* dst = static_cast<float*>(a.dw) + at + 64 * c;
+              vg_store_f32(scr, v[0], dst, a.N, rows, a.add != 0);
+              vg_store_f32(scr, v[1], dst + 32, a.N, rows, a.add != 0);
+            } else {
+              vg_store_bf16(scr, v[0], v[1], static_cast<__nv_bfloat16*>(a.dw) + at + 64 * c, a.N, rows);
+            }
+          }
+        }
+        release();
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();   // no arrival or copy for the other CTA is outstanding
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, 2 * kN);
+    else
+      tmem_dealloc(tmem, 2 * kN);
   }
 }
 
-// The tiles' (max, sum) of 32 tokens joined: 16 lanes of tiles per token, then the lanes in order.
+template <int MODE>
+__global__ void __launch_bounds__(320, 1)
+    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const VgArgs a) {
+  vocab_gemm<MODE, false>(tmA, tmB, a);
+}
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
+    vocab_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const VgArgs a) {
+  vocab_gemm<MODE, true>(tmA, tmB, a);
+}
+
+// The tiles' (max, sum) joined: a block has 4 tokens (one 32-byte sector of `part` a tile) x 128 lanes of tiles,
+// so that a few tokens' thousand tiles are read in a few steps: 34 us with 16 lanes for 7 tokens, now 5.
 __global__ void __launch_bounds__(512) vocab_loss_kernel(const float2* part, int parts, int part_ld, const float* zt,
                                                          Ids targets, int tokens, int vocab, float* loss, float* lse,
                                                          int* err) {
   pdl_wait();
-  __shared__ float2 red[16][32];
-  const int tl = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + tl;
+  __shared__ float2 red[16][4];
+  const int tl = threadIdx.x & 3, g = threadIdx.x >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 4 + tl;
   const bool in = i < tokens;
   float mx = -INFINITY, sum = 0.f;
   auto join = [&](float2 p) {
@@ -380,11 +481,18 @@ __global__ void __launch_bounds__(512) vocab_loss_kernel(const float2* part, int
   };
   if (in) {
 #pragma unroll 8
-    for (int p = g; p < parts; p += 16) join(part[static_cast<int64_t>(p) * part_ld + i]);
+    for (int p = g; p < parts; p += 128) join(part[static_cast<int64_t>(p) * part_ld + i]);
   }
-  red[g][tl] = make_float2(mx, sum);
+#pragma unroll
+  for (int d = 16; d >= 4; d >>= 1) {   // lanes l and l + d hold the same token
+    float2 q;
+    q.x = __shfl_down_sync(0xffffffffu, mx, d);
+    q.y = __shfl_down_sync(0xffffffffu, sum, d);
+    join(q);
+  }
+  if (lane < 4) red[warp][lane] = make_float2(mx, sum);
   __syncthreads();
-  if (g != 0 || !in) return;
+  if (threadIdx.x >= 4 || !in) return;
   for (int k = 1; k < 16; ++k) join(red[k][tl]);
   const float l = mx + logf(sum);
   const int t = targets.get(i);
