@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(256) embed_kernel(const __nv_bfloat16* table, 
 }
 
 // ---------------------------------------------------------------- gradient: positions sorted by id
-constexpr int kEmbTile = 64;        // sorted positions per tile of the sums; a longer segment is cut at tiles
-constexpr int kSortWarps = 32;
-constexpr int kSortMaxRows = 1600;  // vocabulary rows of one sorting CTA: 32 warps x 1600 counters = 200 KB
+constexpr int kEmbTile = 32;        // sorted positions per tile of the sums; a longer segment is cut at tiles
+constexpr int kSortWarps = 16;
+constexpr int kSortMaxRows = 1600;  // vocabulary rows of one sorting CTA: 16 warps x 1600 counters = 100 KB
+constexpr int kSortZero = 1 << 16;  // bytes that one of the sort's zeroing CTAs writes
 
 // Scratch of one gradient.  Sorted place i holds position perm[i] of id row_of[i]; seg[v] is the range of
 // places of id v; total[0] the number of places; long_row[t] the id whose segment of more than kEmbTile
@@ -125,36 +126,65 @@ struct EmbScratch {
 // so the CTAs need no exchange) and its own per (warp, row), warp w taking the w-th stretch of positions;
 // after a scan it writes the positions in (row, position) order.  The ids come from L2: G x n x 8 bytes,
 // twice.  A lane's rank among equal ids of its 32 is counted over the lanes that hold ids of this CTA, few
-// as a rule; match.any took 50 us here for the CTA of the most frequent ids, this 12 us (32768 tokens).
-__global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, int n, int vocab, int log_g, int rows,
-                                                                     EmbScratch o, int* err) {
+// as a rule; match.any in its place took 10 us longer (32768 tokens, 6% of them one id).
+// The sort leaves HBM idle, so the CTAs behind the first G write zeros meanwhile: `zero_bytes` of the gradient
+// from `zero`, the rows of the highest ids, whether their ids occur or not (the sums come later).
+template <typename Id>
+__global__ void __launch_bounds__(kSortWarps * 32, 2) embed_sort_kernel(const Id* ids, int n, int vocab, int log_g, int rows,
+                                                                        EmbScratch o, uint8_t* zero,
+                                                                        int64_t zero_bytes, int* err) {
   extern __shared__ int cnt[];   // [kSortWarps][rows]
   __shared__ int warp_tot[kSortWarps], below_tot[kSortWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int own = blockIdx.x, mask = (1 << log_g) - 1;
+  if (own > mask) {
+    pdl_wait();
+    int64_t at = static_cast<int64_t>(own - mask - 1) * kSortZero + tid * 16;
+#pragma unroll
+    for (int k = 0; k < kSortZero / (kSortWarps * 32 * 16); ++k, at += kSortWarps * 32 * 16)
+      if (at < zero_bytes) __stcs(reinterpret_cast<float4*>(zero + at), make_float4(0.f, 0.f, 0.f, 0.f));
+    return;
+  }
   const int nb = (vocab - own + mask) >> log_g;   // ids own, own + G, ... below vocab
   for (int i = tid; i < kSortWarps * rows; i += blockDim.x) cnt[i] = 0;
   pdl_wait();
   __syncthreads();
   const int chunk = (((n + kSortWarps - 1) / kSortWarps) + 31) & ~31;
-  const int p0 = min(n, warp * chunk), p1 = min(n, p0 + chunk);
-  int* mine = cnt + warp * rows;
+  // the CTAs start at different stretches, or all would ask the same L2 slices at once
+  const int stretch = (warp + own) % kSortWarps;
+  const int p0 = min(n, stretch * chunk), p1 = min(n, p0 + chunk);
+  int* mine = cnt + stretch * rows;
   int below = 0;
   bool bad = false;
-  constexpr int U = 8;
-  for (int b = p0; b < p1; b += 32 * U) {
-    int id[U];
+  // 1024 positions of a warp at a time, all requested together; with up to 16384 tokens one round serves both
+  // passes.  -1: not a token
+  constexpr int U = 32;
+  int id[U];
+  auto fetch = [&](int b) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int p = b + 32 * u + lane;
-      id[u] = p < p1 ? ids.get(p) : -1;
+    for (int u0 = 0; u0 < U; u0 += 16) {
+      if (b + 32 * u0 >= p1) break;
+      Id raw[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int p = b + 32 * (u0 + u) + lane;
+        raw[u] = p < p1 ? __ldg(ids + p) : Id(-1);
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        bad |= raw[u] >= vocab;
+        id[u0 + u] = raw[u] >= 0 && raw[u] < vocab ? static_cast<int>(raw[u]) : -1;
+      }
     }
+  };
+  for (int b = p0; b < p1; b += 32 * U) {
+    fetch(b);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      bad |= id[u] >= vocab;
-      if (id[u] < 0 || id[u] >= vocab) continue;
-      below += (id[u] & mask) < own;
-      if ((id[u] & mask) == own) atomicAdd(&mine[id[u] >> log_g], 1);
+      if (b + 32 * u >= p1) break;
+      const int k = id[u] & mask;
+      if (id[u] >= 0) below += k < own;
+      if (id[u] >= 0 && k == own) atomicAdd(&mine[id[u] >> log_g], 1);
     }
   }
   if (bad && blockIdx.x == 0) raise_error(err, kErrBounds);
@@ -163,14 +193,17 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
   if (lane == 0) below_tot[warp] = below;
   __syncthreads();
   int base = 0;
+#pragma unroll
   for (int w = 0; w < kSortWarps; ++w) base += below_tot[w];
-  // exclusive scan over (row, warp), rows in blocks of 1024
+  // exclusive scan over (row, warp), a row per thread at a time
   int carry = base;
   for (int r0 = 0; r0 < nb; r0 += kSortWarps * 32) {
     const int r = r0 + tid;
     int tot = 0;
-    if (r < nb)
+    if (r < nb) {
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) tot += cnt[w * rows + r];
+    }
     int inc = tot;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -180,6 +213,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
     if (lane == 31) warp_tot[warp] = inc;
     __syncthreads();
     int pre = 0, all = 0;
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
       pre += w < warp ? warp_tot[w] : 0;
       all += warp_tot[w];
@@ -200,15 +234,11 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
   if (tid == 0 && own == mask) o.total[0] = carry;
   if (carry == base) return;   // none of its ids occurs
   for (int b = p0; b < p1; b += 32 * U) {
-    int id[U];
+    if (p1 - p0 > 32 * U) fetch(b);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int p = b + 32 * u + lane;
-      id[u] = p < p1 ? ids.get(p) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = id[u] >= 0 && id[u] < vocab && (id[u] & mask) == own;
+      if (b + 32 * u >= p1) break;
+      const bool in = id[u] >= 0 && (id[u] & mask) == own;
       unsigned act = __ballot_sync(0xffffffffu, in);
       if (!act) continue;
       int rank = 0, same = 0;
@@ -230,50 +260,73 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(Ids ids, in
   }
 }
 
-// Sums of the sorted rows.  Blocks [0, tiles * slices): one tile x 2048 columns, a thread owning 8 columns and
+// eight values as they were loaded, so that a batch of rows waits in half the registers when they are bf16
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&f)[8]) const { bf8_to_f32(q, f); }
+};
+template <>
+struct Raw8<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = v[k];
+  }
+};
+
+// Sums of the sorted rows.  A summing block has one tile x 2048 columns, a thread owning 8 columns and
 // walking the tile's rows, eight requested ahead.  A segment of up to kEmbTile places belongs whole to the tile
-// where it begins (at most 127 rows a tile); a longer one is cut at the tiles and leaves partial sums.  The
-// remaining blocks write the zero rows of ids that never occur (only when the gradient is written, not added to).
+// where it begins (at most 63 rows a tile); a longer one is cut at the tiles and leaves partial sums.  The
+// other blocks write the zero rows of ids below zero_rows that never occur (none when the gradient is added to).
 constexpr int kEmbCols = 2048;   // columns of one block: 256 threads x 8
 constexpr int kEmbZeroRows = 16;
 template <typename Td>
-__global__ void __launch_bounds__(256) embed_sum_kernel(EmbScratch o, const Td* dout, RowsView dv, int vocab, int H,
+__global__ void __launch_bounds__(256, sizeof(Td) == 2 ? 4 : 3) embed_sum_kernel(EmbScratch o, const Td* dout, RowsView dv, int H,
                                                         float scale, float* grad, int accumulate, int tiles,
-                                                        int slices) {
+                                                        int slices, int zero_rows) {
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
-  if (static_cast<int>(blockIdx.x) >= tiles * slices) {
-    const int v0 = (blockIdx.x - tiles * slices) * kEmbZeroRows;
+  // three zeroing blocks behind each summing one, so that the stores of the ones fill the latencies of the others
+  // and no sum begins late
+  const int sums = tiles * slices, b = blockIdx.x;
+  const int step = min(4, static_cast<int>(gridDim.x) / sums);
+  if (b % step != 0 || b / step >= sums) {
+    const int v0 = (b - min(sums, b / step + 1)) * kEmbZeroRows;
     const int my = v0 + (tid & 31);
-    const bool none = (tid & 31) < kEmbZeroRows && my < vocab && o.seg[my].x == o.seg[my].y;
+    const bool none = (tid & 31) < kEmbZeroRows && my < zero_rows && o.seg[my].x == o.seg[my].y;
     for (unsigned todo = __ballot_sync(0xffffffffu, none); todo; todo &= todo - 1) {
       float4* dst = reinterpret_cast<float4*>(grad + static_cast<int64_t>(v0 + __ffs(todo) - 1) * H);
       for (int c = tid; c < H / 4; c += blockDim.x) __stcs(dst + c, make_float4(0.f, 0.f, 0.f, 0.f));
     }
     return;
   }
-  const int tile = blockIdx.x / slices, slice = blockIdx.x - tile * slices;
+  const int tile = b / step / slices, slice = b / step - tile * slices;
   const int m = o.total[0];
   const int i0 = tile * kEmbTile;
   __shared__ int64_t src[2 * kEmbTile];
   __shared__ int row[2 * kEmbTile];
   __shared__ int range[2], cut[2];   // places of this tile; whether its first / last segment is cut
   if (tid == 0) {
-    int a = i0, b = min(m, i0 + kEmbTile), first = 0, last = 0, lrow = -1;
-    if (a < b) {
+    int a = i0, z = min(m, i0 + kEmbTile), first = 0, last = 0, lrow = -1;
+    if (a < z) {
       const int2 g0 = o.seg[o.row_of[a]];
       first = g0.y - g0.x > kEmbTile && g0.x < a;           // goes on from an earlier tile
       if (!first && g0.x < a) a = g0.y;                     // whole in an earlier tile
-      const int v1 = o.row_of[b - 1];
+      const int v1 = o.row_of[z - 1];
       const int2 g1 = o.seg[v1];
       if (g1.y - g1.x > kEmbTile) {
         if (g1.x >= i0) last = 1, lrow = v1;                // begins here, goes on behind
       } else if (g1.x >= i0) {
-        b = g1.y;
+        z = g1.y;
       }
     }
-    range[0] = a, range[1] = b, cut[0] = first, cut[1] = last;
+    range[0] = a, range[1] = z, cut[0] = first, cut[1] = last;
     if (slice == 0) o.long_row[tile] = lrow;
   }
   __syncthreads();
@@ -288,16 +341,18 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbScratch o, const Td* 
   if (c >= H) return;
   float acc[8] = {};
   for (int j0 = 0; j0 < cnt; j0 += 8) {
-    float f[8][8];
+    Raw8<Td> raw[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      if (j0 + u < cnt) load8(dout + src[j0 + u] + c, f[u]);
+      if (j0 + u < cnt) raw[u].load(dout + src[j0 + u] + c);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int j = j0 + u;
       if (j >= cnt) break;
+      float f[8];
+      raw[u].get(f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += f[u][k];
+      for (int k = 0; k < 8; ++k) acc[k] += f[k];
       if (j + 1 < cnt && row[j + 1] == row[j]) continue;
       // the sum of row[j] in this tile is complete
       const bool head = cut[0] && row[j] == row[0], tail = cut[1] && j + 1 == cnt;

@@ -36,7 +36,7 @@ dm0_status rows_ok(dm0_ctx* c, const void* p, int f32, int T, int H, int64_t bat
 }
 
 struct EmbGradPlan {
-  int log_g, rows, tiles, slices, zero_ctas;
+  int log_g, rows, tiles, slices;
   size_t row_of, seg, total, long_row, part, bytes;
 };
 EmbGradPlan emb_grad_plan(int n, int vocab, int H) {
@@ -45,7 +45,6 @@ EmbGradPlan emb_grad_plan(int n, int vocab, int H) {
   p.rows = (vocab + (1 << p.log_g) - 1) >> p.log_g;
   p.tiles = (n + dm0::kEmbTile - 1) / dm0::kEmbTile;
   p.slices = (H + dm0::kEmbCols - 1) / dm0::kEmbCols;
-  p.zero_ctas = (vocab + dm0::kEmbZeroRows - 1) / dm0::kEmbZeroRows;
   p.row_of = align256(sizeof(int) * static_cast<size_t>(n));
   p.seg = 2 * p.row_of;
   p.total = p.seg + align256(sizeof(int2) * static_cast<size_t>(vocab));
@@ -66,10 +65,22 @@ dm0_status embed_grad_run(dm0_ctx* c, cudaStream_t s, dm0::Ids ids, int n, const
   o.total = reinterpret_cast<int*>(ws + p.total);
   o.long_row = reinterpret_cast<int*>(ws + p.long_row);
   o.part = reinterpret_cast<float*>(ws + p.part);
-  TRY(launch(c, s, dm0::embed_sort_kernel, dim3(1 << p.log_g), dim3(dm0::kSortWarps * 32),
-             sizeof(int) * dm0::kSortWarps * p.rows, ids, n, vocab, p.log_g, p.rows, o, c->d_err));
-  TRY(launch(c, s, dm0::embed_sum_kernel<Td>, dim3(p.tiles * p.slices + (accumulate ? 0 : p.zero_ctas)), dim3(256), 0,
-             o, dout, v, vocab, H, scale, grad, accumulate, p.tiles, p.slices));
+  // rows that the sort's shadow has time to zero: about 6 us and 1.2 ns a token, at 5 TB/s
+  const double shadow = (6e-6 + 1.2e-9 * n) * 5e12;
+  const int early = accumulate ? 0 : static_cast<int>(std::min<double>(vocab, shadow / (4.0 * H)));
+  const int64_t zero_bytes = 4ll * H * early;
+  const int zero_rows = accumulate ? 0 : vocab - early;
+  auto sort = [&](auto kernel, auto typed) {
+    return launch(c, s, kernel,
+                  dim3((1 << p.log_g) + static_cast<unsigned>((zero_bytes + dm0::kSortZero - 1) / dm0::kSortZero)),
+                  dim3(dm0::kSortWarps * 32), sizeof(int) * dm0::kSortWarps * p.rows, typed, n, vocab, p.log_g, p.rows,
+                  o, reinterpret_cast<uint8_t*>(grad + static_cast<int64_t>(zero_rows) * H), zero_bytes, c->d_err);
+  };
+  TRY(ids.wide ? sort(dm0::embed_sort_kernel<long long>, static_cast<const long long*>(ids.p))
+               : sort(dm0::embed_sort_kernel<int>, static_cast<const int*>(ids.p)));
+  const int zero_ctas = (zero_rows + dm0::kEmbZeroRows - 1) / dm0::kEmbZeroRows;
+  TRY(launch(c, s, dm0::embed_sum_kernel<Td>, dim3(p.tiles * p.slices + zero_ctas), dim3(256), 0, o, dout, v, H, scale,
+             grad, accumulate, p.tiles, p.slices, zero_rows));
   if (p.tiles < 2) return DM0_OK;   // no segment is longer than a tile
   return launch(c, s, dm0::embed_join_kernel,
                 dim3((p.tiles + dm0::kFixTiles - 1) / dm0::kFixTiles, (H + dm0::kFixCols - 1) / dm0::kFixCols),
@@ -182,10 +193,12 @@ dm0_status vg_tmap(dm0_ctx* c, CUtensorMap* m, const void* p, uint64_t rows, uin
   return r == CUDA_SUCCESS ? DM0_OK : fail(c, DM0_ECUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
 }
 
-// More than 128 tokens: pairs of CTAs on 256 x 256 tiles; up to 128: one CTA on 128 x 256, where a pair's
+// More than 128 tokens: pairs of CTAs on 256 x 256 tiles; up to 128: one CTA on 128 x 128, where a pair's
 // second half of the rows would be padding.
 bool vocab_pairs(int tokens) { return tokens > 128; }
-int vocab_tile_rows(int tokens) { return vocab_pairs(tokens) ? 256 : 128; }
+// token rows of an A k-block's box
+int vocab_a_rows(int tokens) { return std::min(128, (tokens + 7) / 8 * 8); }
+int vocab_tile(int tokens) { return vocab_pairs(tokens) ? 256 : 128; }   // rows and columns
 
 struct VocabLossPlan {
   int mt, nt, part_ld;
@@ -193,8 +206,9 @@ struct VocabLossPlan {
 };
 VocabLossPlan vocab_loss_plan(int tokens, int vocab) {
   VocabLossPlan p{};
-  p.mt = (tokens + vocab_tile_rows(tokens) - 1) / vocab_tile_rows(tokens);
-  p.nt = (vocab + 255) / 256;
+  const int tile = vocab_tile(tokens);
+  p.mt = (tokens + tile - 1) / tile;
+  p.nt = (vocab + tile - 1) / tile;
   p.part_ld = (tokens + 31) / 32 * 32;
   p.part = 0;
   p.zt = align256(sizeof(float2) * 2 * p.nt * static_cast<size_t>(p.part_ld));
@@ -213,8 +227,8 @@ VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
   const int pieces = (vr + most - 1) / most;
   p.piece = ((vr + pieces - 1) / pieces + 255) / 256 * 256;
   // splits of dh's contraction over the piece: whole waves of tiles against the traffic of the fp32 sums
-  const int rows = vocab_tile_rows(tokens), workers = vocab_pairs(tokens) ? kLangSms / 2 : kLangSms;
-  const int64_t tiles = static_cast<int64_t>((tokens + rows - 1) / rows) * ((H + 255) / 256);
+  const int tile = vocab_tile(tokens), workers = vocab_pairs(tokens) ? kLangSms / 2 : kLangSms;
+  const int64_t tiles = static_cast<int64_t>((tokens + tile - 1) / tile) * ((H + tile - 1) / tile);
   const int KB = (std::min(p.piece, vocab) + 63) / 64;   // of the first piece, whose splits all write
   double best = 0;
   for (int S = 1; S <= std::min(KB, 64); ++S) {
@@ -258,8 +272,8 @@ dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   const VocabLossPlan p = vocab_loss_plan(tokens, vocab);
   CUtensorMap ta, tb;
   const bool pairs = vocab_pairs(tokens);
-  TRY(vg_tmap(c, &ta, h, tokens, H, 128));
-  TRY(vg_tmap(c, &tb, w, vocab, H, pairs ? 128 : 256));
+  TRY(vg_tmap(c, &ta, h, tokens, H, vocab_a_rows(tokens)));
+  TRY(vg_tmap(c, &tb, w, vocab, H, 128));
   dm0::VgArgs a{};
   a.M = tokens;
   a.N = vocab;
@@ -268,6 +282,7 @@ dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   a.nt = p.nt;
   a.splits = 1;
   a.kb_per_split = H / 64;
+  a.a_bytes = 128u * vocab_a_rows(tokens);
   a.err = c->d_err;
   a.targets = tgt;
   a.vocab = vocab;
@@ -290,19 +305,20 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   float* part = reinterpret_cast<float*>(ws + p.dh);
   TRY(launch(c, s, dm0::vocab_scale_kernel, dim3(1), dim3(1024), 0, dloss, tgt, tokens, vocab, scale, c->d_err));
   const bool pairs = vocab_pairs(tokens);
-  const int tr = vocab_tile_rows(tokens);
+  const int tile = vocab_tile(tokens);
   CUtensorMap h_k, w_k, g_k, w_mn, g_mn, h_mn;
-  TRY(vg_tmap(c, &h_k, h, tokens, H, 128));
-  TRY(vg_tmap(c, &w_k, w, vocab, H, pairs ? 128 : 256));
-  TRY(vg_tmap(c, &g_k, g, tokens, p.piece, 128));
+  TRY(vg_tmap(c, &h_k, h, tokens, H, vocab_a_rows(tokens)));
+  TRY(vg_tmap(c, &w_k, w, vocab, H, 128));
+  TRY(vg_tmap(c, &g_k, g, tokens, p.piece, vocab_a_rows(tokens)));
   TRY(vg_tmap(c, &w_mn, w, vocab, H, 64));
   TRY(vg_tmap(c, &g_mn, g, tokens, p.piece, 64));
   TRY(vg_tmap(c, &h_mn, h, tokens, H, 64));
-  const int mt = (tokens + tr - 1) / tr, ht = (H + 255) / 256;
+  const int mt = (tokens + tile - 1) / tile, ht = (H + tile - 1) / tile;
   for (int v0 = 0; v0 < vocab; v0 += p.piece) {
     const int cols = std::min(p.piece, vocab - v0);
     dm0::VgArgs a{};
     a.err = c->d_err;
+    a.a_bytes = 128u * vocab_a_rows(tokens);
     a.scale = scale;
     a.vocab = vocab;
     a.v0 = v0;
@@ -311,7 +327,7 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
     a.N = cols;
     a.K = H;
     a.mt = mt;
-    a.nt = (cols + 255) / 256;
+    a.nt = (cols + tile - 1) / tile;
     a.splits = 1;
     a.kb_per_split = H / 64;
     a.b_y0 = v0;
@@ -337,7 +353,8 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
       a.M = cols;
       a.N = H;
       a.K = tokens;
-      a.mt = (cols + tr - 1) / tr;
+      a.a_bytes = 128u * 128u;
+      a.mt = (cols + tile - 1) / tile;
       a.nt = ht;
       a.splits = 1;
       a.kb_per_split = (tokens + 63) / 64;
@@ -378,7 +395,8 @@ bool lang_setup() {
   return norm_grad_setup<f, f, f>() && norm_grad_setup<f, f, bf16>() && norm_grad_setup<f, bf16, f>() &&
          norm_grad_setup<f, bf16, bf16>() && norm_grad_setup<bf16, f, f>() && norm_grad_setup<bf16, f, bf16>() &&
          norm_grad_setup<bf16, bf16, f>() && norm_grad_setup<bf16, bf16, bf16>() &&
-         attr(dm0::embed_sort_kernel, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
+         attr(dm0::embed_sort_kernel<int>, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
+         attr(dm0::embed_sort_kernel<long long>, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
          vocab_setup<dm0::kVgStats>() && vocab_setup<dm0::kVgGrad>() && vocab_setup<dm0::kVgHidden>() &&
          vocab_setup<dm0::kVgWeight>();
 }

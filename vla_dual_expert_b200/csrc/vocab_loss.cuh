@@ -30,6 +30,8 @@ struct VgArgs {
   int mt, nt, splits, kb_per_split;
   int band;             // raster: m-tiles per band (1: n fastest)
   int b_y0;             // offset of B's first row in its map: vocabulary row of the piece
+  uint32_t a_bytes;     // of A's k-block per CTA: with few tokens the box has only their rows, and the tile's others
+                        // are whatever lies in shared memory (rows of a product do not mix; theirs are not stored)
   int* err;
   // statistics and G
   Ids targets;
@@ -48,13 +50,15 @@ struct VgArgs {
   int dw_f32;
 };
 
-// Tile of a CTA, or of a CTA pair (cta_group::2): 128 or 256 rows of A times 256 rows of B.  A pair's CTAs
-// each stage half of A's and of B's rows, so a k-block takes 32 KB of each CTA's shared memory instead of 48.
+// Tile of a CTA pair (cta_group::2): 256 rows of A times 256 rows of B, of which each CTA stages half.  Tile of
+// one CTA, for up to 128 tokens, where a product is one read of W: 128 x 128, narrow so that the tiles of a
+// vocabulary spread evenly (131072 columns, 148 SMs: 7 rounds of 128, 99% busy, against 4 of 256, 86%).
 template <bool PAIR>
 struct VgTile {
-  static constexpr int kM = PAIR ? 256 : 128, kN = 256;
-  static constexpr int kBRows = PAIR ? 128 : 256;   // of B, per CTA
-  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr int kM = PAIR ? 256 : 128, kN = PAIR ? 256 : 128;
+  static constexpr int kBRows = 128;   // of B, per CTA
+  static constexpr int kStages = 6;
+  static constexpr int kStretch = PAIR ? 16 : 8;   // k-blocks of the loss's logits added in the accumulator
   static constexpr uint32_t kA = 128 * 128, kB = kBRows * 128, kStage = kA + kB, kPipe = kStages * kStage;
   static constexpr uint32_t kScr = kPipe;                 // 8 x 4 KB
   static constexpr uint32_t kBar = kScr + 8 * 4096;
@@ -126,7 +130,7 @@ constexpr int kVgStretch = 8;
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const VgArgs& a) {
   using L = VgTile<PAIR>;
-  constexpr int kStages = L::kStages, kN = L::kN;
+  constexpr int kStages = L::kStages, kN = L::kN, kStretch = L::kStretch;
   constexpr bool kAMn = MODE == kVgWeight, kBMn = MODE == kVgHidden || MODE == kVgWeight;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -178,7 +182,7 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
     kb0 = split * a.kb_per_split;
     kb1 = min(KB, kb0 + a.kb_per_split);
   };
-  auto stretch_end = [&](int kb, int kb1) { return MODE == kVgStats ? min(kb1, kb + kVgStretch) : kb1; };
+  auto stretch_end = [&](int kb, int kb1) { return MODE == kVgStats ? min(kb1, kb + kStretch) : kb1; };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -199,7 +203,7 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
           }
           uint8_t* sa = smem + s * L::kStage;
           uint8_t* sb = sa + L::kA;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], PAIR ? 2 * L::kStage : L::kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (a.a_bytes + L::kB));
           const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
           auto load = [&](uint8_t* dst, const CUtensorMap& map, int x, int y) {
             if constexpr (PAIR)

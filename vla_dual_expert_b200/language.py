@@ -53,16 +53,17 @@ class LanguageOps:
         self.device = torch.cuda.current_device()   # the context's: the tensors of these operators live there
         # the raw handle of the current stream, without building a Stream object around it
         self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._place = torch.device("cuda", self.device)
 
     def _on(self, stream):
         if stream is None:
             return self._raw_stream(self.device)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def _scratch(self, like, nbytes: int, stream):
+    def _scratch(self, nbytes: int, stream):
         """Workspace of one call, from torch's allocator, which keeps it from others until the call's stream is past
         it."""
-        ws = like.new_empty(max(nbytes, 16), dtype=torch.uint8)
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self._place)
         if stream is not None:
             ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
                              torch.cuda.ExternalStream(self._on(stream), self.device))
@@ -88,7 +89,7 @@ class LanguageOps:
         tp = _check(table, self.device, (BF16,), tshape, "table")
         oshape = (*shape, H)
         if out is None:
-            out = table.new_empty(oshape)
+            out = torch.empty(*oshape, dtype=BF16, device=self._place)
         bs, rs = _check_rows(out, self.device, oshape, "out")
         st = self.lib.dm0_embed(self.h, tp, ip, wide, 1 if len(shape) == 1 else shape[0], shape[-1], V, H, scale,
                                 out.data_ptr(), out.dtype == F32, bs, rs, self._on(stream))
@@ -107,11 +108,11 @@ class LanguageOps:
         if grad is None:
             if accumulate:
                 raise ValueError("accumulate needs grad")
-            grad = dout.new_empty((vocab, H), dtype=F32)
+            grad = torch.empty(vocab, H, dtype=F32, device=self._place)
         gp = _check(grad, self.device, (F32,), (vocab, H), "grad")
         B, T = 1 if len(shape) == 1 else shape[0], shape[-1]
         n = self.lib.dm0_embed_grad_workspace(B, T, vocab, H)
-        ws = self._scratch(grad, n, stream)
+        ws = self._scratch(n, stream)
         st = self.lib.dm0_embed_grad(self.h, ip, wide, B, T, vocab, H, scale, dout.data_ptr(), dout.dtype == F32, bs, rs,
                                      gp, accumulate, ws.data_ptr(), n, self._on(stream))
         if st:
@@ -165,11 +166,11 @@ class LanguageOps:
         a, hp, yp = self._norm(h, y, post_gain, gate, scale, pre_gain, mod_scale, mod_shift)
         shape = h.shape
         if h_out is None:
-            h_out = h.new_empty(shape)
+            h_out = torch.empty_like(h)
         if n_out is None:
-            n_out = h.new_empty(shape, dtype=BF16)
-        r_pre = h.new_empty(shape[:-1], dtype=F32)
-        r_post = None if post_gain is None else h.new_empty(shape[:-1], dtype=F32)
+            n_out = torch.empty_like(h, dtype=BF16)
+        r_pre = torch.empty(*shape[:-1], dtype=F32, device=self._place)
+        r_post = None if post_gain is None else torch.empty_like(r_pre)
         st = self.lib.dm0_residual_norm(self.h, ctypes.byref(a), hp, yp,
                                         _check(h_out, self.device, (h.dtype,), shape, "h_out"),
                                         _check(n_out, self.device, (BF16,), shape, "n_out"),
@@ -191,20 +192,22 @@ class LanguageOps:
         up = None if dh_out is None else _check(dh_out, dev, (h_out.dtype,), shape, "dh_out")
         rp = _check(r_pre, dev, (F32,), shape[:-1], "r_pre")
         rq = None if r_post is None else _check(r_post, dev, (F32,), shape[:-1], "r_post")
-        out = {"h": h_out.new_empty(shape)}
+        out = {"h": torch.empty_like(h_out)}
         dy = None
         if y is not None:
-            out["y"] = y.new_empty(shape)
+            out["y"] = torch.empty_like(y)
             dy = out["y"].data_ptr()
         ptrs = []
         for name, v in (("post_gain", post_gain), ("gate", gate), ("pre_gain", pre_gain), ("mod_scale", mod_scale),
                         ("mod_shift", mod_shift)):
-            if v is not None:
-                out[name] = v.new_empty(v.shape)
-            ptrs.append(None if v is None else out[name].data_ptr())
+            if v is None:
+                ptrs.append(None)
+            else:
+                out[name] = t = torch.empty_like(v)   # dense: rows that lie apart are not copied in their strides
+                ptrs.append(t.data_ptr())
         g = Dm0NormGrads(*ptrs)
         n = self.lib.dm0_residual_norm_grad_workspace(ctypes.byref(a))
-        ws = self._scratch(h_out, n, stream)
+        ws = self._scratch(n, stream)
         st = self.lib.dm0_residual_norm_grad(self.h, ctypes.byref(a), np_, dn.dtype == F32, up, hp, yp, rq, rp,
                                              out["h"].data_ptr(), dy, ctypes.byref(g), ws.data_ptr(), ws.numel(),
                                              self._on(stream))
@@ -227,9 +230,10 @@ class LanguageOps:
         hidden: bf16 [tokens][H]; weight: bf16 [vocab][H]; targets: int32 or int64 [tokens], negative: no target.
         Returns (loss, lse), f32 [tokens]; -loss is the target's log probability, lse is for vocab_loss_grad."""
         N, V, H, hp, wp, tp, wide = self._vocab(hidden, weight, targets)
-        loss, lse = hidden.new_empty(N, dtype=F32), hidden.new_empty(N, dtype=F32)
+        loss = torch.empty(N, dtype=F32, device=self._place)
+        lse = torch.empty_like(loss)
         n = self.lib.dm0_vocab_loss_workspace(N, V, H)
-        ws = self._scratch(hidden, n, stream)
+        ws = self._scratch(n, stream)
         st = self.lib.dm0_vocab_loss(self.h, hp, wp, tp, wide, N, V, H, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                                      n, self._on(stream))
         if st:
@@ -245,10 +249,10 @@ class LanguageOps:
         N, V, H, hp, wp, tp, wide = self._vocab(hidden, weight, targets)
         if accumulate and not isinstance(dweight, torch.Tensor):
             raise ValueError("accumulate needs dweight")
-        dh, dw = (like.new_empty(like.shape) if t is None else None if t is False else t
+        dh, dw = (torch.empty_like(like) if t is None else None if t is False else t
                   for t, like in ((dhidden, hidden), (dweight, weight)))
         n = self.lib.dm0_vocab_loss_grad_workspace(N, V, H)
-        ws = self._scratch(hidden, n, stream)
+        ws = self._scratch(n, stream)
         st = self.lib.dm0_vocab_loss_grad(
             self.h, hp, wp, tp, wide, _check(lse, self.device, (F32,), (N,), "lse"),
             _check(dloss, self.device, (F32,), (N,), "dloss"), N, V, H,
