@@ -226,16 +226,24 @@ VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
   const int most = std::min(vr, std::max(256, kVgPieceElems / tokens / 256 * 256));
   const int pieces = (vr + most - 1) / most;
   p.piece = ((vr + pieces - 1) / pieces + 255) / 256 * 256;
-  // splits of dh's contraction over the piece: whole waves of tiles against the traffic of the fp32 sums
+  // splits of dh's contraction over the piece: the time of the busiest worker, whose tiles of dh and dW come in
+  // turn (0.28 us a k-block, 1 us a tile), against the traffic of the fp32 sums
   const int tile = vocab_tile(tokens), workers = vocab_pairs(tokens) ? kLangSms / 2 : kLangSms;
-  const int64_t tiles = static_cast<int64_t>((tokens + tile - 1) / tile) * ((H + tile - 1) / tile);
-  const int KB = (std::min(p.piece, vocab) + 63) / 64;   // of the first piece, whose splits all write
+  const int cols = std::min(p.piece, vocab);
+  const int64_t ht = (H + tile - 1) / tile, th = (tokens + tile - 1) / tile * ht, tw = (cols + tile - 1) / tile * ht;
+  const int KB = (cols + 63) / 64, KW = (tokens + 63) / 64;   // of the first piece, whose splits all write
   double best = 0;
   for (int S = 1; S <= std::min(KB, 64); ++S) {
     const int per = (KB + S - 1) / S, used = (KB + per - 1) / per;
     if (used != S) continue;
-    const double t = static_cast<double>((tiles * S + workers - 1) / workers) * (per * 0.28 + 1.0) +
-                     S * 8.0 * tokens * H / 6.0e6;
+    double busiest = 0;
+    // worker 0 has the most tiles of both; the first one with a tile of dh less may have one of dW more
+    for (int64_t w : {int64_t(0), th * S % workers}) {
+      const int64_t mine = (th * S + workers - 1 - w) / workers;
+      const int64_t all = (th * S + tw + workers - 1 - w) / workers;
+      busiest = std::max(busiest, mine * (per * 0.28 + 1.0) + (all - mine) * (KW * 0.28 + 1.0));
+    }
+    const double t = busiest + S * 8.0 * tokens * H / 6.0e6;
     if (S == 1 || t < best) best = t, p.splits = S, p.kb_per_split = per;
   }
   p.scale = 0;
@@ -254,26 +262,30 @@ dm0_status vocab_ok(dm0_ctx* c, const void* h, const void* w, const void* t, int
   return DM0_OK;
 }
 
-template <int MODE>
-dm0_status vocab_gemm(dm0_ctx* c, cudaStream_t s, bool pairs, const CUtensorMap& ta, const CUtensorMap& tb,
-                      const dm0::VgArgs& a) {
-  const int64_t tiles = static_cast<int64_t>(a.mt) * a.nt * a.splits;
+// grid of a product's `tiles`: one CTA per SM, or one pair per two
+dm0_status vocab_grid(dm0_ctx* c, bool pairs, int64_t tiles, dim3* grid) {
   if (tiles > 0x3fffffff) return fail(c, DM0_ESHAPE, "too many tiles");
-  if (pairs)
-    return launch(c, s, dm0::vocab_gemm_pair_kernel<MODE>,
-                  dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms / 2))), dim3(320),
-                  dm0::VgTile<true>::kBytes, ta, tb, a);
-  return launch(c, s, dm0::vocab_gemm_kernel<MODE>, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms))),
-                dim3(320), dm0::VgTile<false>::kBytes, ta, tb, a);
+  *grid = pairs ? dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms / 2)))
+                : dim3(static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms)));
+  return DM0_OK;
+}
+int64_t vocab_tiles(const dm0::VgArgs& a) { return static_cast<int64_t>(a.mt) * a.nt * a.splits; }
+
+template <int MODE>
+dm0_status vocab_gemm(dm0_ctx* c, cudaStream_t s, bool pairs, const dm0::VgMaps& m, const dm0::VgArgs& a) {
+  dim3 grid;
+  TRY(vocab_grid(c, pairs, vocab_tiles(a), &grid));
+  if (pairs) return launch(c, s, dm0::vocab_gemm_pair_kernel<MODE>, grid, dim3(320), dm0::VgTile<true>::kBytes, m, a);
+  return launch(c, s, dm0::vocab_gemm_kernel<MODE>, grid, dim3(320), dm0::VgTile<false>::kBytes, m, a);
 }
 
 dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16* w, dm0::Ids tgt, int tokens, int vocab,
                           int H, float* loss, float* lse, uint8_t* ws) {
   const VocabLossPlan p = vocab_loss_plan(tokens, vocab);
-  CUtensorMap ta, tb;
+  dm0::VgMaps m;
   const bool pairs = vocab_pairs(tokens);
-  TRY(vg_tmap(c, &ta, h, tokens, H, vocab_a_rows(tokens)));
-  TRY(vg_tmap(c, &tb, w, vocab, H, 128));
+  TRY(vg_tmap(c, &m.a, h, tokens, H, vocab_a_rows(tokens)));
+  TRY(vg_tmap(c, &m.b, w, vocab, H, 128));
   dm0::VgArgs a{};
   a.M = tokens;
   a.N = vocab;
@@ -283,6 +295,8 @@ dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   a.splits = 1;
   a.kb_per_split = H / 64;
   a.a_bytes = 128u * vocab_a_rows(tokens);
+  a.b_bytes = 128u * 128u;
+  a.ksteps = 4;
   a.err = c->d_err;
   a.targets = tgt;
   a.vocab = vocab;
@@ -290,9 +304,10 @@ dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.part_ld = p.part_ld;
   a.zt = reinterpret_cast<float*>(ws + p.zt);
-  TRY(vocab_gemm<dm0::kVgStats>(c, s, pairs, ta, tb, a));
+  TRY(vocab_gemm<dm0::kVgStats>(c, s, pairs, m, a));
+  const int parts = 2 * (p.mt > 1 ? p.nt : std::min(p.nt, pairs ? c->num_sms / 2 : c->num_sms));
   return launch(c, s, dm0::vocab_loss_kernel, dim3((tokens + 3) / 4), dim3(512), 0,
-                static_cast<const float2*>(a.part), 2 * p.nt, p.part_ld, static_cast<const float*>(a.zt), tgt, tokens,
+                static_cast<const float2*>(a.part), parts, p.part_ld, static_cast<const float*>(a.zt), tgt, tokens,
                 vocab, loss, lse, c->d_err);
 }
 
@@ -303,26 +318,27 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   float* scale = reinterpret_cast<float*>(ws + p.scale);
   bf16* g = reinterpret_cast<bf16*>(ws + p.g);
   float* part = reinterpret_cast<float*>(ws + p.dh);
-  TRY(launch(c, s, dm0::vocab_scale_kernel, dim3(1), dim3(1024), 0, dloss, tgt, tokens, vocab, scale, c->d_err));
   const bool pairs = vocab_pairs(tokens);
   const int tile = vocab_tile(tokens);
-  CUtensorMap h_k, w_k, g_k, w_mn, g_mn, h_mn;
-  TRY(vg_tmap(c, &h_k, h, tokens, H, vocab_a_rows(tokens)));
-  TRY(vg_tmap(c, &w_k, w, vocab, H, 128));
-  TRY(vg_tmap(c, &g_k, g, tokens, p.piece, vocab_a_rows(tokens)));
-  TRY(vg_tmap(c, &w_mn, w, vocab, H, 64));
-  TRY(vg_tmap(c, &g_mn, g, tokens, p.piece, 64));
-  TRY(vg_tmap(c, &h_mn, h, tokens, H, 64));
+  dm0::VgMaps mg, mh, mw;   // operands of G, dh and dW
+  TRY(vg_tmap(c, &mg.a, h, tokens, H, vocab_a_rows(tokens)));
+  TRY(vg_tmap(c, &mg.b, w, vocab, H, 128));
+  TRY(vg_tmap(c, &mh.a, g, tokens, p.piece, vocab_a_rows(tokens)));
+  TRY(vg_tmap(c, &mh.b, w, vocab, H, 64));
+  const int kbox = std::min(64, (tokens + 15) / 16 * 16);   // tokens of a k-block of dW
+  TRY(vg_tmap(c, &mw.a, g, tokens, p.piece, kbox));
+  TRY(vg_tmap(c, &mw.b, h, tokens, H, kbox));
   const int mt = (tokens + tile - 1) / tile, ht = (H + tile - 1) / tile;
   for (int v0 = 0; v0 < vocab; v0 += p.piece) {
     const int cols = std::min(p.piece, vocab - v0);
-    dm0::VgArgs a{};
+    dm0::VgArgs a{};   // G of the piece
     a.err = c->d_err;
     a.a_bytes = 128u * vocab_a_rows(tokens);
+    a.b_bytes = 128u * 128u;
+    a.ksteps = 4;
     a.scale = scale;
     a.vocab = vocab;
     a.v0 = v0;
-    // G of the piece
     a.M = tokens;
     a.N = cols;
     a.K = H;
@@ -337,34 +353,35 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
     a.dloss = dloss;
     a.g = g;
     a.ldg = p.piece;
-    TRY(vocab_gemm<dm0::kVgGrad>(c, s, pairs, h_k, w_k, a));
-    if (dh) {
-      a.N = H;
-      a.K = cols;
-      a.nt = ht;
-      a.kb_per_split = p.kb_per_split;
-      a.splits = ((cols + 63) / 64 + p.kb_per_split - 1) / p.kb_per_split;
-      a.band = 1;
-      a.dh = part;
-      a.add = v0 > 0;
-      TRY(vocab_gemm<dm0::kVgHidden>(c, s, pairs, g_k, w_mn, a));
-    }
-    if (dw) {
-      a.M = cols;
-      a.N = H;
-      a.K = tokens;
-      a.a_bytes = 128u * 128u;
-      a.mt = (cols + tile - 1) / tile;
-      a.nt = ht;
-      a.splits = 1;
-      a.kb_per_split = (tokens + 63) / 64;
-      a.band = 1;
-      a.b_y0 = 0;
-      a.add = accumulate;
-      a.dw = dw;
-      a.dw_f32 = dw_f32;
-      TRY(vocab_gemm<dm0::kVgWeight>(c, s, pairs, g_mn, h_mn, a));
-    }
+    TRY(vocab_gemm<dm0::kVgGrad>(c, s, pairs, mg, a));
+    dm0::VgArgs ah = a, aw = a;
+    ah.N = H;
+    ah.K = cols;
+    ah.nt = dh ? ht : 0;
+    ah.kb_per_split = p.kb_per_split;
+    ah.splits = ((cols + 63) / 64 + p.kb_per_split - 1) / p.kb_per_split;
+    ah.band = 1;
+    ah.dh = part;
+    ah.add = v0 > 0;
+    aw.M = cols;
+    aw.N = H;
+    aw.K = tokens;
+    aw.a_bytes = aw.b_bytes = 2u * 128u * kbox;   // two boxes of 64 columns
+    aw.ksteps = kbox / 16;
+    aw.mt = (cols + tile - 1) / tile;
+    aw.nt = dw ? ht : 0;
+    aw.kb_per_split = (tokens + 63) / 64;
+    aw.band = 1;
+    aw.b_y0 = 0;
+    aw.add = accumulate;
+    aw.dw = dw;
+    aw.dw_f32 = dw_f32;
+    dim3 grid;
+    TRY(vocab_grid(c, pairs, vocab_tiles(ah) + vocab_tiles(aw), &grid));
+    if (pairs)
+      TRY(launch(c, s, dm0::vocab_back_pair_kernel, grid, dim3(320), dm0::VgTile<true>::kBytes, mh, ah, mw, aw));
+    else
+      TRY(launch(c, s, dm0::vocab_back_kernel, grid, dim3(320), dm0::VgTile<false>::kBytes, mh, ah, mw, aw));
   }
   if (!dh) return DM0_OK;
   const int64_t n = static_cast<int64_t>(tokens) * H;
@@ -378,14 +395,6 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
                 static_cast<const float*>(scale), static_cast<bf16*>(dh));
 }
 
-template <int MODE>
-bool vocab_setup() {
-  return cudaFuncSetAttribute(dm0::vocab_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              dm0::VgTile<false>::kBytes) == cudaSuccess &&
-         cudaFuncSetAttribute(dm0::vocab_gemm_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              dm0::VgTile<true>::kBytes) == cudaSuccess;
-}
-
 // shared-memory limits of these kernels (dm0_create)
 bool lang_setup() {
   auto attr = [](auto kernel, int bytes) {
@@ -397,8 +406,12 @@ bool lang_setup() {
          norm_grad_setup<bf16, bf16, f>() && norm_grad_setup<bf16, bf16, bf16>() &&
          attr(dm0::embed_sort_kernel<int>, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
          attr(dm0::embed_sort_kernel<long long>, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
-         vocab_setup<dm0::kVgStats>() && vocab_setup<dm0::kVgGrad>() && vocab_setup<dm0::kVgHidden>() &&
-         vocab_setup<dm0::kVgWeight>();
+         attr(dm0::vocab_gemm_kernel<dm0::kVgStats>, dm0::VgTile<false>::kBytes) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgGrad>, dm0::VgTile<false>::kBytes) &&
+         attr(dm0::vocab_back_kernel, dm0::VgTile<false>::kBytes) &&
+         attr(dm0::vocab_gemm_pair_kernel<dm0::kVgStats>, dm0::VgTile<true>::kBytes) &&
+         attr(dm0::vocab_gemm_pair_kernel<dm0::kVgGrad>, dm0::VgTile<true>::kBytes) &&
+         attr(dm0::vocab_back_pair_kernel, dm0::VgTile<true>::kBytes);
 }
 }  // namespace
 

@@ -7,8 +7,9 @@
 // One tcgen05 kernel does all four products; its mode sets the operands' majors and the epilogue:
 //   kVgStats  z tile -> the row's (max, sum of exp) of its columns, and z_{i, t_i}
 //   kVgGrad   z tile again -> G / s in bf16, one piece of the vocabulary at a time
-//   kVgHidden dh += G W   of the piece: A = G (K-major), B = W read along H (MN-major), fp32 sums
-//   kVgWeight dW  = G^T h of the piece: A = G read along V (MN-major), B = h read along H (MN-major)
+//   kVgBack   both products with the piece's G, in one launch:
+//             dh += G W:  A = G (K-major), B = W read along H (MN-major), fp32 sums
+//             dW = G^T h: A = G read along V (MN-major), B = h read along H (MN-major)
 //
 // s = max |dloss_i| over the tokens with a target: G / s is what is rounded to bf16 and s multiplies the
 // fp32 results, so the factor 1 / tokens of a mean, the same in every row, takes no part in the rounding
@@ -23,24 +24,30 @@
 
 namespace dm0 {
 
-enum VgMode : int { kVgStats = 0, kVgGrad = 1, kVgHidden = 2, kVgWeight = 3 };
+enum VgMode : int { kVgStats = 0, kVgGrad = 1, kVgBack = 2 };
 
 struct VgArgs {
   int M, N, K;          // of this product (rows of A, rows of B, contraction)
   int mt, nt, splits, kb_per_split;
   int band;             // raster: m-tiles per band (1: n fastest)
   int b_y0;             // offset of B's first row in its map: vocabulary row of the piece
-  uint32_t a_bytes;     // of A's k-block per CTA: with few tokens the box has only their rows, and the tile's others
-                        // are whatever lies in shared memory (rows of a product do not mix; theirs are not stored)
+  // Bytes of A's and B's k-block per CTA.  Rows that a box takes beyond its tensor cost the copy engine as much as
+  // others, so with few tokens the boxes have only theirs: as rows of A, the tile's others are then whatever lies
+  // in shared memory (rows of a product do not mix; theirs are not stored); as the contraction of dW, to the next
+  // multiple of 16, and ksteps instructions of 16 take no more.
+  uint32_t a_bytes, b_bytes;
+  int ksteps;
   int* err;
   // statistics and G
   Ids targets;
   int vocab, v0;        // whole vocabulary; first column of the piece
   int valid_n;          // columns of this product that are vocabulary entries
-  float2* part;         // [2 nt][part_ld] (max, sum) of each tile half
+  float2* part;         // (max, sum): [2 nt][part_ld] of each tile half; with one m-tile, where a worker's tiles
+                        // have the same rows, [2 workers][part_ld] of its halves of all of them
   int part_ld;
   float* zt;            // [tokens] logit of the target
-  const float *lse, *dloss, *scale;   // scale[0] = s
+  const float *lse, *dloss;
+  float* scale;         // scale[0] = s: found by the first piece's kVgGrad, read by the others
   __nv_bfloat16* g;     // [tokens][ldg]
   int ldg;
   // dh: fp32 sums of the splits, [split][tokens][H]; dW: rows of the piece
@@ -58,6 +65,7 @@ struct VgTile {
   static constexpr int kM = PAIR ? 256 : 128, kN = PAIR ? 256 : 128;
   static constexpr int kBRows = 128;   // of B, per CTA
   static constexpr int kStages = 6;
+  static constexpr int kBufs = 512 / kN;   // accumulators in TMEM
   static constexpr int kStretch = PAIR ? 16 : 8;   // k-blocks of the loss's logits added in the accumulator
   static constexpr uint32_t kA = 128 * 128, kB = kBRows * 128, kStage = kA + kB, kPipe = kStages * kStage;
   static constexpr uint32_t kScr = kPipe;                 // 8 x 4 KB
@@ -124,35 +132,42 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kVgStretch = 8;
 
 // Warp 0: TMA; warp 1: TMEM and, in a pair's first CTA, MMA; warps 2..9: epilogue, two per TMEM lane quarter
-// (column halves).  Persistent: one CTA per SM, or one pair per two, walks the tiles; the accumulator is
-// double-buffered.  In a pair the copies of both CTAs count on the first one's `full`, its MMAs free both
+// (column halves; sixteen warps on quarters, with stores of 64 instead of 128 bytes a row, made the gradients of
+// 8192 tokens 10.9 ms instead of 10.0).  Persistent: one CTA per SM, or one pair per two, walks the tiles; the accumulator is
+// buffered (two of a pair, four of a CTA), and free again
+// as soon as it is in registers.  In a pair the copies of both CTAs count on the first one's `full`, its MMAs free both
 // CTAs' stages and fill both accumulators, and both epilogues free its `tempty`.
+// kVgBack's tiles: dh's first, then dW's, each product with its own operands.
+struct VgMaps {
+  CUtensorMap a, b;
+};
 template <int MODE, bool PAIR>
-__device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtensorMap& tmB, const VgArgs& a) {
+__device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, const VgMaps& m1, const VgArgs& a1) {
   using L = VgTile<PAIR>;
-  constexpr int kStages = L::kStages, kN = L::kN, kStretch = L::kStretch;
-  constexpr bool kAMn = MODE == kVgWeight, kBMn = MODE == kVgHidden || MODE == kVgWeight;
+  constexpr int kStages = L::kStages, kN = L::kN, kBufs = L::kBufs, kStretch = L::kStretch;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + kBufs;
+  uint64_t* drain = tempty + kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* red = reinterpret_cast<float*>(tmem_slot + 2);   // [8]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_rank()) : 0;
   const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
-  const int KB = (a.K + 63) >> 6;
-  const int plane = a.mt * a.nt, ntiles = plane * a.splits;
+  int* const err = a0.err;
+  const int tiles0 = a0.mt * a0.nt * a0.splits;
+  const int ntiles = MODE == kVgBack ? tiles0 + a1.mt * a1.nt * a1.splits : tiles0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], PAIR ? 16 : 8);
     }
@@ -162,9 +177,9 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
   }
   if (warp == 1) {
     if constexpr (PAIR) {
-      tmem_alloc_pair(tmem_slot, 2 * kN);
+      tmem_alloc_pair(tmem_slot, kBufs * kN);
     } else {
-      tmem_alloc(tmem_slot, 2 * kN);
+      tmem_alloc(tmem_slot, kBufs * kN);
       tmem_relinquish();
     }
   }
@@ -176,34 +191,52 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
   pdl_launch_dependents();
   pdl_wait();
 
-  auto tile_at = [&](int t, int& m, int& n, int& kb0, int& kb1, int& split) {
-    split = t / plane;
-    band_tile(t - split * plane, a.mt, a.nt, a.band, m, n);
-    kb0 = split * a.kb_per_split;
-    kb1 = min(KB, kb0 + a.kb_per_split);
+  struct Tile {
+    bool second;   // of kVgBack: a tile of dW
+    int m, n, kb0, kb1, split;
+  };
+  auto tile_at = [&](int t) {
+    Tile w;
+    w.second = MODE == kVgBack && t >= tiles0;
+    const VgArgs& a = w.second ? a1 : a0;
+    if (w.second) t -= tiles0;
+    const int plane = a.mt * a.nt;
+    w.split = t / plane;
+    band_tile(t - w.split * plane, a.mt, a.nt, a.band, w.m, w.n);
+    w.kb0 = w.split * a.kb_per_split;
+    w.kb1 = min((a.K + 63) >> 6, w.kb0 + a.kb_per_split);
+    return w;
   };
   auto stretch_end = [&](int kb, int kb1) { return MODE == kVgStats ? min(kb1, kb + kStretch) : kb1; };
 
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&tmA);
-      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&m0.a);
+      tma_prefetch_desc(&m0.b);
+      if (MODE == kVgBack) {
+        tma_prefetch_desc(&m1.a);
+        tma_prefetch_desc(&m1.b);
+      }
       const uint64_t keep = policy_evict_last();
       int it = 0;
       for (int t = worker; t < ntiles && !*abort_flag; t += workers) {
-        int m, n, kb0, kb1, split;
-        tile_at(t, m, n, kb0, kb1, split);
-        const int ra = m * L::kM + rank * 128, rb = n * kN + rank * L::kBRows;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const Tile w = tile_at(t);
+        const VgArgs& a = w.second ? a1 : a0;
+        const VgMaps& maps = w.second ? m1 : m0;
+        const bool a_mn = w.second, b_mn = MODE == kVgBack;
+        const int ra = w.m * L::kM + rank * 128, rb = w.n * kN + rank * L::kBRows;
+        const uint32_t bytes = (PAIR ? 2 : 1) * (a.a_bytes + a.b_bytes);
+        const int by0 = a.b_y0;
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
           const int s = it % kStages;
           if (it >= kStages && !mbar_wait(&empty[s], ((it / kStages) - 1) & 1, abort_flag)) {
             *abort_flag = 1;
-            raise_error(a.err, kErrTimeoutProducer);
+            raise_error(err, kErrTimeoutProducer);
             break;
           }
           uint8_t* sa = smem + s * L::kStage;
           uint8_t* sb = sa + L::kA;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * (a.a_bytes + L::kB));
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
           auto load = [&](uint8_t* dst, const CUtensorMap& map, int x, int y) {
             if constexpr (PAIR)
@@ -211,17 +244,17 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
             else
               tma_load_2d(dst, &map, &full[s], x, y, keep);
           };
-          if constexpr (kAMn) {
+          if (a_mn) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) load(sa + 8192 * j, tmA, ra + 64 * j, kb * 64);
+            for (int j = 0; j < 2; ++j) load(sa + 8192 * j, maps.a, ra + 64 * j, kb * 64);
           } else {
-            load(sa, tmA, kb * 64, ra);
+            load(sa, maps.a, kb * 64, ra);
           }
-          if constexpr (kBMn) {
+          if (b_mn) {
 #pragma unroll
-            for (int j = 0; j < L::kBRows / 64; ++j) load(sb + 8192 * j, tmB, rb + 64 * j, a.b_y0 + kb * 64);
+            for (int j = 0; j < L::kBRows / 64; ++j) load(sb + 8192 * j, maps.b, rb + 64 * j, by0 + kb * 64);
           } else {
-            load(sb, tmB, kb * 64, a.b_y0 + rb);
+            load(sb, maps.b, kb * 64, by0 + rb);
           }
         }
       }
@@ -230,12 +263,11 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
       if (rank == 0)
         for (int i = it - kStages; i < it; ++i) {
           if (i < 0) continue;
-          if (!mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, kDrainTimeoutNs)) raise_error(a.err, kErrDrain);
+          if (!mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, kDrainTimeoutNs)) raise_error(err, kErrDrain);
         }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_bf16_f32(L::kM, kN) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
       auto commit = [&](uint64_t* bar) {
         if constexpr (PAIR)
           umma_commit_pair(bar);
@@ -245,12 +277,15 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
       int it = 0, local = 0;
       bool ok = true;
       for (int t = worker; ok && t < ntiles; t += workers) {
-        int m, n, kb0, kb1, split;
-        tile_at(t, m, n, kb0, kb1, split);
-        for (int ks = kb0; ok && ks < kb1; ++local) {
-          const int ke = stretch_end(ks, kb1), buf = local & 1;
-          const uint32_t freed = ((local >> 1) - 1) & 1;
-          if (local >= 2 && !(PAIR ? mbar_wait_cluster(&tempty[buf], freed, abort_flag)
+        const Tile w = tile_at(t);
+        const bool a_mn = w.second;
+        constexpr bool b_mn = MODE == kVgBack;
+        const int ksteps = (w.second ? a1 : a0).ksteps;
+        const uint32_t idesc = idesc_bf16_f32(L::kM, kN) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        for (int ks = w.kb0; ok && ks < w.kb1; ++local) {
+          const int ke = stretch_end(ks, w.kb1), buf = local % kBufs;
+          const uint32_t freed = (local / kBufs - 1) & 1;
+          if (local >= kBufs && !(PAIR ? mbar_wait_cluster(&tempty[buf], freed, abort_flag)
                                    : mbar_wait(&tempty[buf], freed, abort_flag))) {
             ok = false;
             break;
@@ -266,8 +301,9 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
             const uint32_t aa = smem_u32(smem + s * L::kStage), bb = aa + L::kA;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t da = kAMn ? sw128_mnmajor_desc(aa + 2048 * kk, 8192) : sw128_kmajor_desc(aa + 32 * kk);
-              const uint64_t db = kBMn ? sw128_mnmajor_desc(bb + 2048 * kk, 8192) : sw128_kmajor_desc(bb + 32 * kk);
+              if (MODE == kVgBack && kk >= ksteps) break;
+              const uint64_t da = a_mn ? sw128_mnmajor_desc(aa + 2048 * kk, 8192) : sw128_kmajor_desc(aa + 32 * kk);
+              const uint64_t db = b_mn ? sw128_mnmajor_desc(bb + 2048 * kk, 8192) : sw128_kmajor_desc(bb + 32 * kk);
               const uint32_t acc = (kb > ks || kk != 0) ? 1u : 0u;
               if constexpr (PAIR)
                 umma_bf16_pair(tmem + buf * kN, da, db, idesc, acc);
@@ -282,24 +318,47 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
       }
       if (!ok) {
         *abort_flag = 1;
-        raise_error(a.err, kErrTimeoutMma);
+        raise_error(err, kErrTimeoutMma);
       }
       commit(drain);
-      if (!mbar_wait(drain, 0, nullptr, kWaitTimeoutNs + kDrainTimeoutNs)) raise_error(a.err, kErrDrain);
+      if (!mbar_wait(drain, 0, nullptr, kWaitTimeoutNs + kDrainTimeoutNs)) raise_error(err, kErrDrain);
     }
   } else {
     const int lane_base = (warp & 3) * 32, half = (warp - 2) >> 2;
     uint8_t* scr = smem + L::kScr + (warp - 2) * 4096;
     constexpr int kCols = kN / 2;   // columns of this warp
-    const float s = MODE == kVgGrad || MODE == kVgWeight ? a.scale[0] : 1.f;
+    float s = 1.f;
+    if constexpr (MODE == kVgGrad) {
+      if (a0.v0 == 0) {   // s, by every CTA beside its first tile's products; the first one keeps it
+        float mx = 0.f;
+        bool bad = false;
+        for (int i = threadIdx.x - 64; i < a0.M; i += 256) {
+          const int t = a0.targets.get(i);
+          bad |= t >= a0.vocab;
+          if (t >= 0 && t < a0.vocab) mx = fmaxf(mx, fabsf(a0.dloss[i]));
+        }
+        if (bad && blockIdx.x == 0) raise_error(err, kErrBounds);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        if (lane == 0) red[warp - 2] = mx;
+        named_bar_sync(1, 256);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx = fmaxf(mx, red[k]);
+        s = mx > 0.f ? mx : 1.f;
+        if (blockIdx.x == 0 && threadIdx.x == 64) a0.scale[0] = s;
+      } else {
+        s = a0.scale[0];
+      }
+    }
+    if constexpr (MODE == kVgBack) s = a0.scale[0];
     int local = 0;
     auto ready = [&]() {   // the next accumulator of this CTA is complete
-      if (mbar_wait(&tfull[local & 1], (local >> 1) & 1, abort_flag)) {
+      if (mbar_wait(&tfull[local % kBufs], (local / kBufs) & 1, abort_flag)) {
         tc_fence_after();
         return true;
       }
       *abort_flag = 1;
-      raise_error(a.err, kErrTimeoutEpilogue);
+      raise_error(err, kErrTimeoutEpilogue);
       return false;
     };
     auto release = [&]() {   // and read
@@ -307,29 +366,30 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR)
-          mbar_arrive_cluster(cluster_addr(&tempty[local & 1], 0));
+          mbar_arrive_cluster(cluster_addr(&tempty[local % kBufs], 0));
         else
-          mbar_arrive(&tempty[local & 1]);
+          mbar_arrive(&tempty[local % kBufs]);
       }
       ++local;
     };
     const uint32_t tm0 = tmem + (static_cast<uint32_t>(lane_base) << 16) + half * kCols;
     bool go = true;
+    float run_mx = -INFINITY, run_sum = 0.f;   // of kVgStats with one m-tile
     for (int t = worker; go && t < ntiles; t += workers) {
-      int m, n, kb0, kb1, split;
-      tile_at(t, m, n, kb0, kb1, split);
-      const int row0 = m * L::kM + rank * 128 + lane_base, row = row0 + lane;
-      const int col0 = n * kN + half * kCols;
+      const Tile w = tile_at(t);
+      const VgArgs& a = w.second ? a1 : a0;
+      const int row0 = w.m * L::kM + rank * 128 + lane_base, row = row0 + lane;
+      const int col0 = w.n * kN + half * kCols;
       const int rows = min(32, a.M - row0);   // rows of this warp to store (may be <= 0)
       if constexpr (MODE == kVgStats) {
         float v[kCols / 32][32];
-        for (int ks = kb0; ks < kb1; ks = stretch_end(ks, kb1)) {
+        for (int ks = w.kb0; ks < w.kb1; ks = stretch_end(ks, w.kb1)) {
           if (!ready()) {
             go = false;
             break;
           }
-          const uint32_t tm = tm0 + (local & 1) * kN;
-          if (ks == kb0) {
+          const uint32_t tm = tm0 + (local % kBufs) * kN;
+          if (ks == w.kb0) {
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tm + 32 * c, v[c]);
           } else {
@@ -365,18 +425,23 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
             for (int j = 0; j < 32; ++j) z = tgt - col0 == 32 * c + j ? v[c][j] : z;
           a.zt[row] = z;
         }
+        mx = fmaxf(mx, run_mx);
         const float ref = mx == -INFINITY ? 0.f : mx * kLog2e;
-        float sum[4] = {};
+        float sum[4] = {run_sum * ex2_fast(run_mx * kLog2e - ref), 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[j & 3] += ex2_fast(fmaf(v[c][j], kLog2e, -ref));
-        if (row < a.M)
-          a.part[static_cast<int64_t>(2 * n + half) * a.part_ld + row] =
-              make_float2(mx, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        const float2 now = make_float2(mx, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (a.mt > 1) {
+          if (row < a.M) a.part[static_cast<int64_t>(2 * w.n + half) * a.part_ld + row] = now;
+        } else {
+          run_mx = now.x, run_sum = now.y;
+          if (t + workers >= ntiles && row < a.M) a.part[static_cast<int64_t>(2 * worker + half) * a.part_ld + row] = now;
+        }
       } else {
         if (!ready()) break;
-        const uint32_t tm = tm0 + (local & 1) * kN;
+        const uint32_t tm = tm0 + (local % kBufs) * kN;
         if constexpr (MODE == kVgGrad) {
           int tgt = -1;
           float l2 = 0.f, gi = 0.f;
@@ -393,6 +458,7 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               tmem_ld32(tm + 64 * c + 32 * q, v[q]);
+              if (c + 1 == kCols / 64 && q == 1) release();
               const int cc = col0 + 64 * c + 32 * q;
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[q][j] = ex2_fast(fmaf(v[q][j], kLog2e, -l2)) * gi;
@@ -409,12 +475,13 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
             }
             vg_store_bf16(scr, v[0], v[1], a.g + static_cast<int64_t>(row0) * a.ldg + col0 + 64 * c, a.ldg, rows);
           }
-        } else if constexpr (MODE == kVgHidden) {
-          float* dst = a.dh + (static_cast<int64_t>(split) * a.M + row0) * a.N + col0;
+        } else if (!w.second) {
+          float* dst = a.dh + (static_cast<int64_t>(w.split) * a.M + row0) * a.N + col0;
 #pragma unroll 1
           for (int c = 0; c < kCols / 32; ++c) {
             float v[32];
             tmem_ld32(tm + 32 * c, v);
+            if (c + 1 == kCols / 32) release();
             if (col0 + 32 * c < a.N) vg_store_f32(scr, v, dst + 32 * c, a.N, rows, a.add != 0);
           }
         } else {
@@ -424,6 +491,7 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
             float v[2][32];
             tmem_ld32(tm + 64 * c, v[0]);
             tmem_ld32(tm + 64 * c + 32, v[1]);
+            if (c + 1 == kCols / 64) release();
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -438,7 +506,6 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
             }
           }
         }
-        release();
       }
     }
   }
@@ -448,34 +515,46 @@ __device__ __forceinline__ void vocab_gemm(const CUtensorMap& tmA, const CUtenso
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR)
-      tmem_dealloc_pair(tmem, 2 * kN);
+      tmem_dealloc_pair(tmem, kBufs * kN);
     else
-      tmem_dealloc(tmem, 2 * kN);
+      tmem_dealloc(tmem, kBufs * kN);
   }
 }
 
 template <int MODE>
 __global__ void __launch_bounds__(320, 1)
-    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const VgArgs a) {
-  vocab_gemm<MODE, false>(tmA, tmB, a);
+    vocab_gemm_kernel(const __grid_constant__ VgMaps m, const __grid_constant__ VgArgs a) {
+  vocab_gemm<MODE, false>(m, a, m, a);
 }
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
-    vocab_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                           const VgArgs a) {
-  vocab_gemm<MODE, true>(tmA, tmB, a);
+    vocab_gemm_pair_kernel(const __grid_constant__ VgMaps m, const __grid_constant__ VgArgs a) {
+  vocab_gemm<MODE, true>(m, a, m, a);
+}
+__global__ void __launch_bounds__(320, 1)
+    vocab_back_kernel(const __grid_constant__ VgMaps mh, const __grid_constant__ VgArgs ah,
+                      const __grid_constant__ VgMaps mw, const __grid_constant__ VgArgs aw) {
+  vocab_gemm<kVgBack, false>(mh, ah, mw, aw);
+}
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
+    vocab_back_pair_kernel(const __grid_constant__ VgMaps mh, const __grid_constant__ VgArgs ah,
+                           const __grid_constant__ VgMaps mw, const __grid_constant__ VgArgs aw) {
+  vocab_gemm<kVgBack, true>(mh, ah, mw, aw);
 }
 
 // The tiles' (max, sum) joined: a block has 4 tokens (one 32-byte sector of `part` a tile) x 128 lanes of tiles,
-// so that a few tokens' thousand tiles are read in a few steps: 34 us with 16 lanes for 7 tokens, now 5.
+// so that a few tokens' thousand tiles are read in a few steps (7 tokens: 34 us with 16 lanes, 6 with 128).
 __global__ void __launch_bounds__(512) vocab_loss_kernel(const float2* part, int parts, int part_ld, const float* zt,
                                                          Ids targets, int tokens, int vocab, float* loss, float* lse,
                                                          int* err) {
-  pdl_wait();
   __shared__ float2 red[16][4];
   const int tl = threadIdx.x & 3, g = threadIdx.x >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.x * 4 + tl;
   const bool in = i < tokens;
+  const int t = in ? targets.get(i) : -1;
+  pdl_wait();
+  const bool held = t >= 0 && t < vocab;
+  const float z = held && threadIdx.x < 4 ? zt[i] : 0.f;
   float mx = -INFINITY, sum = 0.f;
   auto join = [&](float2 p) {
     const float m = fmaxf(mx, p.x);
@@ -483,49 +562,32 @@ __global__ void __launch_bounds__(512) vocab_loss_kernel(const float2* part, int
     sum = sum * expf(mx - ref) + p.y * expf(p.x - ref);
     mx = m;
   };
+  auto join_lanes = [&]() {   // lanes l and l + d hold the same token
+#pragma unroll
+    for (int d = 16; d >= 4; d >>= 1) {
+      float2 q;
+      q.x = __shfl_down_sync(0xffffffffu, mx, d);
+      q.y = __shfl_down_sync(0xffffffffu, sum, d);
+      join(q);
+    }
+  };
   if (in) {
 #pragma unroll 8
     for (int p = g; p < parts; p += 128) join(part[static_cast<int64_t>(p) * part_ld + i]);
   }
-#pragma unroll
-  for (int d = 16; d >= 4; d >>= 1) {   // lanes l and l + d hold the same token
-    float2 q;
-    q.x = __shfl_down_sync(0xffffffffu, mx, d);
-    q.y = __shfl_down_sync(0xffffffffu, sum, d);
-    join(q);
-  }
+  join_lanes();
   if (lane < 4) red[warp][lane] = make_float2(mx, sum);
   __syncthreads();
-  if (threadIdx.x >= 4 || !in) return;
-  for (int k = 1; k < 16; ++k) join(red[k][tl]);
+  if (warp != 0) return;
+  mx = -INFINITY, sum = 0.f;
+  join(red[lane >> 2][tl]);
+  join(red[8 + (lane >> 2)][tl]);
+  join_lanes();
+  if (lane >= 4 || !in) return;
   const float l = mx + logf(sum);
-  const int t = targets.get(i);
   if (t >= vocab) raise_error(err, kErrBounds);
   lse[i] = l;
-  loss[i] = t >= 0 && t < vocab ? l - zt[i] : 0.f;
-}
-
-// s of the header comment: max |dloss| over the tokens with a target, 1 if that is 0
-__global__ void __launch_bounds__(1024) vocab_scale_kernel(const float* dloss, Ids targets, int tokens, int vocab,
-                                                           float* scale, int* err) {
-  pdl_wait();
-  __shared__ float red[32];
-  float m = 0.f;
-  bool bad = false;
-  for (int i = threadIdx.x; i < tokens; i += blockDim.x) {
-    const int t = targets.get(i);
-    bad |= t >= vocab;
-    if (t >= 0 && t < vocab) m = fmaxf(m, fabsf(dloss[i]));
-  }
-  if (bad) raise_error(err, kErrBounds);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < 32; ++k) m = fmaxf(m, red[k]);
-    scale[0] = m > 0.f ? m : 1.f;
-  }
+  loss[i] = held ? l - z : 0.f;
 }
 
 // dh = s * the sum of the splits, in order
@@ -537,6 +599,7 @@ __global__ void __launch_bounds__(256) vocab_hidden_kernel(const float* part, in
   if (i >= n) return;
   const float s = scale[0];
   float f[8] = {};
+#pragma unroll 8
   for (int k = 0; k < splits; ++k) {
     float p[8];
     load8_rw(part + k * n + i, p);
