@@ -144,3 +144,76 @@ def test_vocab_workspaces(abi):
     assert 0 < small < large < 4096 * 131072   # no logits
     grad = lib.dm0_vocab_loss_grad_workspace(8192, 131072, 2048)
     assert 0 < grad < 2 ** 30 < 2 * 8192 * 131072
+
+
+# ------------------------------------------------------------------------------ the binding's own checks (no GPU)
+@pytest.fixture(scope="module")
+def ops():
+    """The operators' argument handling, on CPU tensors: their get_device() is -1, which stands for the context's."""
+    from vla_dual_expert_b200 import language
+    language._bind()
+    o = language.LanguageOps()
+    o.device = -1
+    return language, o
+
+
+def test_binding_refuses_types_shapes_and_strides(ops):
+    import torch
+    lang, o = ops
+    t = torch.zeros(3, 4, 16)
+    f32 = (torch.float32,)
+    assert lang._check(t, -1, f32, (3, 4, 16), "t") == t.data_ptr()
+    for bad in (t.double(), t.transpose(0, 1).contiguous().transpose(0, 1)):
+        with pytest.raises(TypeError):
+            lang._check(bad, -1, f32, (3, 4, 16), "t")
+    with pytest.raises(TypeError):
+        lang._check(t, 0, f32, (3, 4, 16), "t")        # another device
+    with pytest.raises(ValueError):
+        lang._check(t, -1, f32, (3, 4, 15), "t")
+    assert lang._check_rows(t[:, 1:3], -1, (3, 2, 16), "t") == (64, 16)
+    assert lang._check_rows(t[:1, 1:2], -1, (1, 1, 16), "t") == (0, 16)   # strides of dimensions of one say nothing
+    assert lang._check_rows(t.transpose(0, 1), -1, (4, 3, 16), "t") == (16, 64)
+    with pytest.raises(ValueError):
+        lang._check_rows(t.transpose(1, 2), -1, (3, 16, 4), "t")
+    with pytest.raises(TypeError):
+        lang._check_rows(t.half(), -1, (3, 4, 16), "t")
+    with pytest.raises(ValueError):
+        o._ids(torch.zeros(2, 2, 2, dtype=torch.int64))
+    with pytest.raises(TypeError):
+        o._ids(torch.zeros(2, 2))
+
+
+def test_binding_vectors_per_sample(ops):
+    import torch
+    _, o = ops
+    m = torch.zeros(3, 40)
+    assert o._vector(None, 3, 16, "v") == (None, 0)
+    assert o._vector(m[0, :16], 3, 16, "v")[1] == 0
+    assert o._vector(m[:, 8:24], 3, 16, "v") == (m.data_ptr() + 32, 40)   # rows of a wider table
+    assert o._vector(m[:1, :16], 1, 16, "v")[1] == 0
+    with pytest.raises(ValueError):
+        o._vector(m[:2, :16], 3, 16, "v")
+    with pytest.raises(ValueError):
+        o._vector(m[0, :16].expand(3, 16), 3, 16, "v")     # one row seen three times: its gradient would have none
+    with pytest.raises(TypeError):
+        o._vector(m.double()[0, :16], 3, 16, "v")
+    h = torch.zeros(3, 2, 16)
+    with pytest.raises(ValueError):
+        o._norm(h, None, None, None, 1.0, None, m[:, :16], torch.zeros(3, 16))   # scale and shift laid out differently
+    with pytest.raises(ValueError):
+        o._norm(h, torch.zeros(3, 2, 8), None, None, 1.0, None, None, None)
+    with pytest.raises(ValueError):
+        o._norm(torch.zeros(16), None, None, None, 1.0, None, None, None)
+
+
+def test_binding_accumulation_needs_a_gradient(ops):
+    import torch
+    _, o = ops
+    ids, d = torch.zeros(2, dtype=torch.int64), torch.zeros(2, 16)
+    with pytest.raises(ValueError):
+        o.embed_grad(ids, d, 4, accumulate=True)
+    h, w, l = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(5, 64, dtype=torch.bfloat16), torch.zeros(2)
+    with pytest.raises(ValueError):
+        o.vocab_loss_grad(h, w, ids, l, l, accumulate=True)
+    with pytest.raises(ValueError):
+        o.vocab_loss(h, torch.zeros(5, 128, dtype=torch.bfloat16), ids)

@@ -97,6 +97,17 @@ class LanguageOps:
             self._chk(st)
         return out
 
+    def prefill_tokens(self, image_emb, table, ids, scale: float = 1.0):
+        """Prefix pass over [image rows; text rows] on the current stream: image_emb CUDA bf16 [B][Ti][hidden_v], and
+        the table's rows of ids [B][Tt] behind them.  Returns the prefix it passed to prefill, [B][Ti + Tt][hidden_v]."""
+        B, Ti, H = image_emb.shape
+        _check_rows(image_emb, self.device, (B, Ti, H), "image_emb")
+        prefix = torch.empty(B, Ti + ids.shape[-1], H, dtype=BF16, device=self._place)
+        prefix[:, :Ti] = image_emb
+        self.embed(table, ids, scale, out=prefix[:, Ti:])
+        self.prefill(prefix)
+        return prefix
+
     def embed_grad(self, ids, dout, vocab: int, scale: float = 1.0, grad=None, accumulate: bool = False, stream=None):
         """Gradient of embed with respect to its table (dm0_embed_grad): f32 [vocab][hidden].
 
