@@ -149,71 +149,62 @@ def test_vocab_workspaces(abi):
 # ------------------------------------------------------------------------------ the binding's own checks (no GPU)
 @pytest.fixture(scope="module")
 def ops():
-    """The operators' argument handling, on CPU tensors: their get_device() is -1, which stands for the context's."""
+    """The operators of an Engine without a context: every call here is refused by the native binding before it."""
+    build.build()
     from vla_dual_expert_b200 import language
     language._bind()
     o = language.LanguageOps()
-    o.device = -1
-    return language, o
+    o.device, o.h = 0, ctypes.c_void_p()
+    return o
 
 
-def test_binding_refuses_types_shapes_and_strides(ops):
+def _cpu():
     import torch
-    lang, o = ops
-    t = torch.zeros(3, 4, 16)
-    f32 = (torch.float32,)
-    assert lang._check(t, -1, f32, (3, 4, 16), "t") == t.data_ptr()
-    for bad in (t.double(), t.transpose(0, 1).contiguous().transpose(0, 1)):
-        with pytest.raises(TypeError):
-            lang._check(bad, -1, f32, (3, 4, 16), "t")
-    with pytest.raises(TypeError):
-        lang._check(t, 0, f32, (3, 4, 16), "t")        # another device
-    with pytest.raises(ValueError):
-        lang._check(t, -1, f32, (3, 4, 15), "t")
-    assert lang._check_rows(t[:, 1:3], -1, (3, 2, 16), "t") == (64, 16)
-    assert lang._check_rows(t[:1, 1:2], -1, (1, 1, 16), "t") == (0, 16)   # strides of dimensions of one say nothing
-    assert lang._check_rows(t.transpose(0, 1), -1, (4, 3, 16), "t") == (16, 64)
-    with pytest.raises(ValueError):
-        lang._check_rows(t.transpose(1, 2), -1, (3, 16, 4), "t")
-    with pytest.raises(TypeError):
-        lang._check_rows(t.half(), -1, (3, 4, 16), "t")
-    with pytest.raises(ValueError):
-        o._ids(torch.zeros(2, 2, 2, dtype=torch.int64))
-    with pytest.raises(TypeError):
-        o._ids(torch.zeros(2, 2))
+    bf, f32, i64 = torch.bfloat16, torch.float32, torch.int64
+    return dict(table=torch.zeros(9, 64, dtype=bf), ids=torch.zeros(2, 3, dtype=i64), d=torch.zeros(2, 3, 64),
+                h=torch.zeros(2, 3, 64), g=torch.zeros(64), m=torch.zeros(2, 64), x=torch.zeros(5, 64, dtype=bf),
+                t=torch.zeros(5, dtype=i64), l=torch.zeros(5), r=torch.zeros(2, 3, dtype=f32))
 
 
-def test_binding_vectors_per_sample(ops):
+def test_binding_refuses_host_tensors(ops):
+    c = _cpu()
+    for call in (lambda: ops.embed(c["table"], c["ids"]), lambda: ops.embed_grad(c["ids"], c["d"], 9),
+                 lambda: ops.residual_norm(c["h"]), lambda: ops.vocab_loss(c["x"], c["table"], c["t"]),
+                 lambda: ops.residual_norm_grad(c["h"], None, c["h"], None, None, c["r"]),
+                 lambda: ops.vocab_loss_grad(c["x"], c["table"], c["t"], c["l"], c["l"])):
+        with pytest.raises(TypeError, match="cuda:0"):
+            call()
+
+
+def test_binding_refuses_what_is_no_tensor(ops):
+    c = _cpu()
+    with pytest.raises(TypeError, match="table must be a tensor"):
+        ops.embed([1.0], c["ids"])
+    with pytest.raises(TypeError, match="ids must be a tensor"):
+        ops.embed(c["table"], [0, 1])
+    with pytest.raises(TypeError, match="r_pre must be a tensor"):
+        ops.residual_norm_grad(c["h"], None, c["h"], None, None, None)
+    with pytest.raises(TypeError):
+        ops.vocab_loss(c["x"], c["table"], None)
+
+
+def test_binding_refuses_shapes(ops):
     import torch
-    _, o = ops
-    m = torch.zeros(3, 40)
-    assert o._vector(None, 3, 16, "v") == (None, 0)
-    assert o._vector(m[0, :16], 3, 16, "v")[1] == 0
-    assert o._vector(m[:, 8:24], 3, 16, "v") == (m.data_ptr() + 32, 40)   # rows of a wider table
-    assert o._vector(m[:1, :16], 1, 16, "v")[1] == 0
+    c = _cpu()
+    with pytest.raises(ValueError, match="ids must be"):
+        ops.embed(c["table"], torch.zeros(2, 2, 2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="hidden must be"):
+        ops.vocab_loss(c["x"], torch.zeros(9, 128, dtype=torch.bfloat16), c["t"])
+    with pytest.raises(ValueError, match="hidden must be"):
+        ops.vocab_loss(c["x"][0], c["table"], c["t"])
+    with pytest.raises(ValueError, match="residual stream"):
+        ops.residual_norm(torch.zeros(64))
     with pytest.raises(ValueError):
-        o._vector(m[:2, :16], 3, 16, "v")
-    with pytest.raises(ValueError):
-        o._vector(m[0, :16].expand(3, 16), 3, 16, "v")     # one row seen three times: its gradient would have none
-    with pytest.raises(TypeError):
-        o._vector(m.double()[0, :16], 3, 16, "v")
-    h = torch.zeros(3, 2, 16)
-    with pytest.raises(ValueError):
-        o._norm(h, None, None, None, 1.0, None, m[:, :16], torch.zeros(3, 16))   # scale and shift laid out differently
-    with pytest.raises(ValueError):
-        o._norm(h, torch.zeros(3, 2, 8), None, None, 1.0, None, None, None)
-    with pytest.raises(ValueError):
-        o._norm(torch.zeros(16), None, None, None, 1.0, None, None, None)
+        ops.prefill_tokens(torch.zeros(2, 4, 64, dtype=torch.bfloat16), c["table"], c["ids"][:1])
 
 
-def test_binding_accumulation_needs_a_gradient(ops):
-    import torch
-    _, o = ops
-    ids, d = torch.zeros(2, dtype=torch.int64), torch.zeros(2, 16)
-    with pytest.raises(ValueError):
-        o.embed_grad(ids, d, 4, accumulate=True)
-    h, w, l = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(5, 64, dtype=torch.bfloat16), torch.zeros(2)
-    with pytest.raises(ValueError):
-        o.vocab_loss_grad(h, w, ids, l, l, accumulate=True)
-    with pytest.raises(ValueError):
-        o.vocab_loss(h, torch.zeros(5, 128, dtype=torch.bfloat16), ids)
+def test_binding_counts_its_arguments(ops):
+    from vla_dual_expert_b200 import _language
+    for name in ("embed", "embed_grad", "residual_norm", "residual_norm_grad", "vocab_loss", "vocab_loss_grad"):
+        with pytest.raises(TypeError, match="expected"):
+            getattr(_language, name)(0, 0)

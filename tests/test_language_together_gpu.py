@@ -206,6 +206,24 @@ def test_refusals_leave_the_context_usable(eng):  # noqa: F811
         eng.embed(table[:, :60].contiguous(), ids)
     with pytest.raises(TypeError):
         eng.embed(table.cpu(), ids)
+    f = torch.zeros(3, 40, device="cuda")
+    h, gain = torch.zeros(3, 2, 16, device="cuda"), torch.ones(16, device="cuda")
+    for bad in (dict(gate=f[:2, :16]), dict(gate=f[0, :16].expand(3, 16)), dict(y=h[:, :1]), dict(pre_gain=gain[:8]),
+                dict(mod_scale=f[:, :16], mod_shift=torch.zeros(3, 16, device="cuda"))):
+        with pytest.raises(ValueError):
+            eng.residual_norm(h, **{"y": h, **bad})
+    for bad in (dict(gate=f.double()[:, :16]), dict(y=h.half()), dict(pre_gain=gain.cpu()), dict(h_out=h.bfloat16()),
+                dict(post_gain=torch.ones(32, device="cuda")[::2]), dict(y=h.transpose(0, 1).contiguous().transpose(0, 1))):
+        with pytest.raises(TypeError):
+            eng.residual_norm(h, **{"y": h, **bad})
+    with pytest.raises(ValueError):
+        eng.embed_grad(ids, torch.zeros(3, 64, device="cuda"), 10, accumulate=True)
+    with pytest.raises(ValueError):
+        eng.embed_grad(ids, torch.zeros(4, 64, device="cuda"), 10)
+    with pytest.raises(ValueError):
+        eng.embed_grad(ids, torch.zeros(64, 3, device="cuda").t(), 10)   # rows that are not contiguous
+    with pytest.raises(ValueError):
+        eng.embed(table, ids, out=torch.zeros(3, 32, device="cuda"))
     with pytest.raises(TypeError):
         eng.embed(table.t(), ids)
     with pytest.raises(Dm0Error):

@@ -1,18 +1,22 @@
-"""Build libdm0.so (the C-ABI library) in-tree for sm_100a with nvcc.
+"""Build libdm0.so (the C-ABI library) in-tree for sm_100a with nvcc, and _language.so (the native binding of the
+language operators, against the installed torch) with g++.
 
     python -m vla_dual_expert_b200.build [--force] [--ptxas-verbose]
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libdm0.so")
+BINDING = os.path.join(HERE, "_language.so")
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(HERE, "csrc")
 
@@ -33,7 +37,38 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
+def _binding_sources():
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "dm0.h")]
+
+
+def build_binding(force: bool = False) -> str:
+    """_language.so; needs libdm0.so, which it links against (found beside it)."""
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING)
+                                                     for s in _binding_sources()):
+        return BINDING
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++20", "-fPIC", "-shared",
+           "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp",
+           "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+           "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
+    build_library(force, ptxas_verbose)
+    build_binding(force)
+    return LIB
+
+
+def build_library(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     cmd = [nvcc_path(), "-O3", "-std=c++17",
