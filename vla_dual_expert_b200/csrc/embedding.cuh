@@ -418,4 +418,156 @@ __global__ void __launch_bounds__(256) embed_join_kernel(EmbScratch o, int tiles
   }
 }
 
+// ---------------------------------------------------------------- gradient of few tokens in one launch
+// The same sums for up to kEmbFew tokens: each owner lists its tokens in order (their places among the list's equal
+// ids by comparing with the entries before, of which there are n / G as a rule), adds them, and writes the zero
+// rows of its own ids, so that nothing waits for another launch.  A warp adds up to kEmbTile rows of one id and 256
+// columns; a longer segment is cut as above and its partials joined by the same block.
+// One launch against three, at 4500 rows of 1232 (32003 of 1024): 48 tokens 8 against 18 us (23 against 27), 256
+// tokens 12 against 18 (23 against 27).  The price is one block's bandwidth for a frequent id: 256 tokens of one
+// id 33 against 18 us (41 against 29), 512 already 55 (59), so more tokens take the three launches.
+constexpr int kEmbFew = 256;
+template <typename Id, typename Td>
+__global__ void __launch_bounds__(512, 1) embed_few_kernel(const Id* ids, int n, int vocab, int log_g, int rows,
+                                                           const Td* dout, RowsView dv, int H, float scale, float* grad,
+                                                           int accumulate, float* part, int* err) {
+  extern __shared__ int bins[];   // [rows + 1] first places
+  __shared__ int2 listed[kEmbFew], sorted[kEmbFew];   // (row, position)
+  __shared__ int piece[kEmbFew], pieces;              // places where a piece begins, and their number
+  __shared__ int warp_n[16], below_n[16], scan[16];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int own = blockIdx.x, mask = (1 << log_g) - 1;
+  const int nb = max(0, (vocab - own + mask) >> log_g);
+  for (int i = tid; i <= rows; i += 512) bins[i] = 0;
+  pdl_wait();
+  const Id raw = tid < n ? __ldg(ids + tid) : Id(-1);   // a position per thread
+  const bool bad = raw >= vocab;
+  const int v = raw >= 0 && raw < vocab ? static_cast<int>(raw) : -1;
+  int below = v >= 0 && (v & mask) < own;
+  const int id = v >= 0 && (v & mask) == own ? v >> log_g : -1;
+  const unsigned act = __ballot_sync(0xffffffffu, id >= 0);
+  if (bad && own == 0) raise_error(err, kErrBounds);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xffffffffu, below, d);
+  if (lane == 0) warp_n[warp] = __popc(act), below_n[warp] = below;
+  __syncthreads();
+  int base = 0, at = 0, m = 0;   // places of smaller owners; this warp's first entry; entries
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    base += below_n[w];
+    at += w < warp ? warp_n[w] : 0;
+    m += warp_n[w];
+  }
+  if (id >= 0) {
+    listed[at + __popc(act & ((1u << lane) - 1u))] = make_int2(id, tid);
+    atomicAdd(&bins[id], 1);
+  }
+  __syncthreads();
+  // bins: counts -> first places, kept beside the next row's as the segment's end
+  int carry = 0;
+  for (int r0 = 0; r0 < nb; r0 += 512) {
+    const int r = r0 + tid, k = r < nb ? bins[r] : 0;
+    int inc = k;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int pre = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      pre += w < warp ? scan[w] : 0;
+      all += scan[w];
+    }
+    if (r < nb) bins[r] = carry + pre + inc - k;
+    carry += all;
+    __syncthreads();
+  }
+  if (tid == 0) bins[nb] = m;
+  if (tid < m) {
+    const int2 e = listed[tid];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < tid; ++j) rank += listed[j].x == e.x;
+    sorted[bins[e.x] + rank] = e;
+  }
+  __syncthreads();
+  // the pieces: at each segment's first place and every kEmbTile places on
+  const bool begins = tid < m && (tid - bins[sorted[tid].x]) % kEmbTile == 0;
+  const unsigned beg = __ballot_sync(0xffffffffu, begins);
+  if (lane == 0) warp_n[warp] = __popc(beg);
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) before += w < warp ? warp_n[w] : 0;
+  if (begins) piece[before + __popc(beg & ((1u << lane) - 1u))] = tid;
+  if (tid == 511) pieces = before + __popc(beg);
+  __syncthreads();
+  const int chunks = (H + 255) / 256;
+  auto slot = [&](int i) {   // of the cut piece that begins at place i: segments are told apart by their first piece
+    return static_cast<int64_t>((base + i) / kEmbTile) * 2 + (i == bins[sorted[i].x] ? 1 : 0);
+  };
+  for (int t = warp; t < pieces * chunks; t += 16) {
+    const int k0 = t / chunks, c = (t - k0 * chunks) * 256 + lane * 8;
+    if (c >= H) continue;
+    const int i = piece[k0], r = sorted[i].x, len = min(kEmbTile, bins[r + 1] - i);
+    const bool whole = bins[r + 1] - bins[r] <= kEmbTile;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < len; j0 += 8) {
+      Raw8<Td> raw8[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (j0 + u < len) raw8[u].load(dout + dv.off(sorted[i + j0 + u].y) + c);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (j0 + u >= len) break;
+        float f[8];
+        raw8[u].get(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += f[k];
+      }
+    }
+    if (whole) {
+      float* dst = grad + ((static_cast<int64_t>(r) << log_g) + own) * H + c;
+      float d[8] = {};
+      if (accumulate) load8_rw(dst, d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] = accumulate ? d[k] + scale * acc[k] : scale * acc[k];
+      store8(dst, d);
+    } else {
+      store8(part + slot(i) * H + c, acc);
+    }
+  }
+  if (!accumulate)
+    for (int r = warp; r < nb; r += 16) {
+      if (bins[r] != bins[r + 1]) continue;
+      float4* dst = reinterpret_cast<float4*>(grad + ((static_cast<int64_t>(r) << log_g) + own) * H);
+      for (int c = lane; c < H / 4; c += 32) __stcs(dst + c, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  if (m <= kEmbTile) return;   // nothing was cut
+  __syncthreads();
+  for (int i = 0; i < m;) {
+    const int r = sorted[i].x, end = bins[r + 1];
+    if (end - i > kEmbTile)
+      for (int c = tid * 4; c < H; c += 2048) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int j = i; j < end; j += kEmbTile) {
+          const float4 p = *reinterpret_cast<const float4*>(part + slot(j) * H + c);
+          s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+        }
+        float4* dst = reinterpret_cast<float4*>(grad + ((static_cast<int64_t>(r) << log_g) + own) * H + c);
+        float4 d = make_float4(scale * s.x, scale * s.y, scale * s.z, scale * s.w);
+        if (accumulate) {
+          const float4 old = *dst;
+          d = make_float4(d.x + old.x, d.y + old.y, d.z + old.z, d.w + old.w);
+        }
+        *dst = d;
+      }
+    i = end;
+  }
+}
+
 }  // namespace dm0

@@ -65,6 +65,14 @@ dm0_status embed_grad_run(dm0_ctx* c, cudaStream_t s, dm0::Ids ids, int n, const
   o.total = reinterpret_cast<int*>(ws + p.total);
   o.long_row = reinterpret_cast<int*>(ws + p.long_row);
   o.part = reinterpret_cast<float*>(ws + p.part);
+  if (n <= dm0::kEmbFew) {
+    auto few = [&](auto kernel, auto typed) {
+      return launch(c, s, kernel, dim3(1 << p.log_g), dim3(512), sizeof(int) * (p.rows + 1), typed, n, vocab, p.log_g, p.rows,
+                    dout, v, H, scale, grad, accumulate, o.part, c->d_err);
+    };
+    return ids.wide ? few(dm0::embed_few_kernel<long long, Td>, static_cast<const long long*>(ids.p))
+                    : few(dm0::embed_few_kernel<int, Td>, static_cast<const int*>(ids.p));
+  }
   // rows that the sort's shadow has time to zero: about 6 us and 1.2 ns a token, at 5 TB/s
   const double shadow = (6e-6 + 1.2e-9 * n) * 5e12;
   const int early = accumulate ? 0 : static_cast<int>(std::min<double>(vocab, shadow / (4.0 * H)));
