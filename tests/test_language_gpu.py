@@ -497,6 +497,19 @@ def test_vocab_loss_rows_without_a_target(eng):
     assert (dh == 0).all() and (dw == 0).all()
 
 
+def test_vocab_loss_grad_keeps_infinities_in_their_rows(eng):
+    """A weight of infinity or NaN on one token reaches that token's dhidden and no other's."""
+    h, w, t = loss_case(rng(17), 40, 300, 64, missing=0.0)
+    _, lse = eng.vocab_loss(h, w, t)
+    dl = torch.full((40,), 0.3, device="cuda")
+    want, _ = eng.vocab_loss_grad(h, w, t, lse, dl)
+    dl[7], dl[21] = float("inf"), float("nan")
+    got, dw = eng.vocab_loss_grad(h, w, t, lse, dl)
+    keep = [i for i in range(40) if i not in (7, 21)]
+    assert torch.equal(got[keep], want[keep])
+    assert not torch.isfinite(got[7]).any() and got[21].isnan().all() and dw.isnan().all()
+
+
 def test_vocab_loss_extreme_logits(eng):
     """Logits of +-1000s: the maximum is taken out before the exponentials."""
     N, V, H = 130, 600, 64

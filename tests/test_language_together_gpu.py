@@ -73,8 +73,8 @@ def test_captured_steps_replay_and_do_not_share_scratch(eng):  # noqa: F811
         s.run()
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
-            outs.append(s.run())
+        with torch.cuda.graph(g):   # the capturing stream named once, once not
+            outs.append(s.run(stream=torch.cuda.current_stream() if s is a else None))
         graphs.append(g)
     for s in (a, b):    # new inputs in the captured tensors
         s.ids.copy_(torch.where(s.ids < 0, 1, s.ids.flip(-1)))

@@ -57,6 +57,7 @@ struct Call {
   int device;
   PyObject* given;   // the stream argument
   cudaStream_t stream;
+  bool foreign = false;   // not torch's current stream, which the allocator goes by
 
   Call(PyObject* const* args, PyObject* stream_arg) : given(stream_arg) {
     ctx = static_cast<dm0_ctx*>(PyLong_AsVoidPtr(args[0]));
@@ -66,18 +67,16 @@ struct Call {
   }
   // after the tensors' checks: nothing before needs a GPU
   void open() {
-    if (given == Py_None) {
-      stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
-    } else {
-      stream = static_cast<cudaStream_t>(PyLong_AsVoidPtr(given));
-      if (PyErr_Occurred()) throw PyErr();
-    }
+    const cudaStream_t current = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+    stream = given == Py_None ? current : static_cast<cudaStream_t>(PyLong_AsVoidPtr(given));
+    if (PyErr_Occurred()) throw PyErr();
+    foreign = stream != current;
   }
   // a tensor of torch's allocator; on a stream that is not torch's current one it is kept until that is past it
   Tensor make(at::IntArrayRef shape, ScalarType kind) const {
     Tensor t = at::detail::empty_cuda(shape, kind,
                                       c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)), std::nullopt);
-    if (given != Py_None && t.numel())
+    if (foreign && t.numel())
       c10::cuda::CUDACachingAllocator::recordStream(
           t.storage().data_ptr(),
           c10::cuda::getStreamFromExternal(stream, static_cast<c10::DeviceIndex>(device)));

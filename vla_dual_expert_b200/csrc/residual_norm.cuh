@@ -172,7 +172,7 @@ template <typename Tn, typename Th, typename Ty, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1)
     residual_norm_grad_kernel(const Tn* dn, const Th* dh_out, const Th* h_out, const Ty* y, RnGradArgs a, Th* dh,
                               Ty* dy) {
-  extern __shared__ uint8_t ring[];   // [stages][h_out | dh_out | dn | y] rows
+  extern __shared__ __align__(16) uint8_t ring[];   // [stages][h_out | dh_out | dn | y] rows
   __shared__ uint64_t full[kRnMaxStages];
   __shared__ float4 red[2][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5;

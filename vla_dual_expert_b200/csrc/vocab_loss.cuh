@@ -11,7 +11,7 @@
 //             dh += G W:  A = G (K-major), B = W read along H (MN-major), fp32 sums
 //             dW = G^T h: A = G read along V (MN-major), B = h read along H (MN-major)
 //
-// s = max |dloss_i| over the tokens with a target: G / s is what is rounded to bf16 and s multiplies the
+// s = max |dloss_i|, of the finite ones of the tokens with a target: G / s is what is rounded to bf16 and s multiplies the
 // fp32 results, so the factor 1 / tokens of a mean, the same in every row, takes no part in the rounding
 // (a constant dloss that is no power of two would otherwise put one and the same relative error of up to
 // 2^-8 / 2 into every entry -dloss of the targets, which no sum averages out).
@@ -335,7 +335,8 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
         for (int i = threadIdx.x - 64; i < a0.M; i += 256) {
           const int t = a0.targets.get(i);
           bad |= t >= a0.vocab;
-          if (t >= 0 && t < a0.vocab) mx = fmaxf(mx, fabsf(a0.dloss[i]));
+          const float d = fabsf(a0.dloss[i]);
+          if (t >= 0 && t < a0.vocab && d <= 3.402823466e38f) mx = fmaxf(mx, d);   // infinities and NaN stay in their rows
         }
         if (bad && blockIdx.x == 0) raise_error(err, kErrBounds);
 #pragma unroll
