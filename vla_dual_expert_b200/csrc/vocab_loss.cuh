@@ -21,6 +21,7 @@
 #include "attention_tc.cuh"   // sw128_mnmajor_desc
 #include "embedding.cuh"
 #include "gemm.cuh"           // band_tile, resid_swz, bf2
+#include "residual_norm.cuh"  // store4
 
 namespace dm0 {
 
@@ -195,7 +196,9 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
     bool second;   // of kVgBack: a tile of dW
     int m, n, kb0, kb1, split;
   };
-  auto tile_at = [&](int t) {
+  const int mine = worker < ntiles ? (ntiles - 1 - worker) / workers + 1 : 0;   // tiles of this worker
+  auto tile_at = [&](int q) {
+    int t = worker + q * workers;
     Tile w;
     w.second = MODE == kVgBack && t >= tiles0;
     const VgArgs& a = w.second ? a1 : a0;
@@ -219,8 +222,8 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
       }
       const uint64_t keep = policy_evict_last();
       int it = 0;
-      for (int t = worker; t < ntiles && !*abort_flag; t += workers) {
-        const Tile w = tile_at(t);
+      for (int q = 0; q < mine && !*abort_flag; ++q) {
+        const Tile w = tile_at(q);
         const VgArgs& a = w.second ? a1 : a0;
         const VgMaps& maps = w.second ? m1 : m0;
         const bool a_mn = w.second, b_mn = MODE == kVgBack;
@@ -276,8 +279,8 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
       };
       int it = 0, local = 0;
       bool ok = true;
-      for (int t = worker; ok && t < ntiles; t += workers) {
-        const Tile w = tile_at(t);
+      for (int q = 0; ok && q < mine; ++q) {
+        const Tile w = tile_at(q);
         const bool a_mn = w.second;
         constexpr bool b_mn = MODE == kVgBack;
         const int ksteps = (w.second ? a1 : a0).ksteps;
@@ -376,12 +379,20 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
     const uint32_t tm0 = tmem + (static_cast<uint32_t>(lane_base) << 16) + half * kCols;
     bool go = true;
     float run_mx = -INFINITY, run_sum = 0.f;   // of kVgStats with one m-tile
-    for (int t = worker; go && t < ntiles; t += workers) {
-      const Tile w = tile_at(t);
+    for (int q = 0; go && q < mine; ++q) {
+      const Tile w = tile_at(q);
       const VgArgs& a = w.second ? a1 : a0;
       const int row0 = w.m * L::kM + rank * 128 + lane_base, row = row0 + lane;
       const int col0 = w.n * kN + half * kCols;
       const int rows = min(32, a.M - row0);   // rows of this warp to store (may be <= 0)
+      // what the epilogue knows of its row, requested while the products run
+      int tgt = -1;
+      float row_lse = 0.f, row_dloss = 0.f;
+      if (MODE != kVgBack && row < a.M) {
+        tgt = a.targets.get(row);
+        if (tgt >= a.vocab) tgt = -1;
+        if (MODE == kVgGrad) row_lse = a.lse[row], row_dloss = a.dloss[row];
+      }
       if constexpr (MODE == kVgStats) {
         float v[kCols / 32][32];
         for (int ks = w.kb0; ks < w.kb1; ks = stretch_end(ks, w.kb1)) {
@@ -405,7 +416,6 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           release();
         }
         if (!go) break;
-        const int tgt = row < a.M ? a.targets.get(row) : -1;
         if (col0 + kCols > a.valid_n) {
 #pragma unroll
           for (int c = 0; c < kCols / 32; ++c)
@@ -418,7 +428,7 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
         for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
           for (int j = 0; j < 32; j += 2) mx = max3f(mx, v[c][j], v[c][j + 1]);
-        if (static_cast<unsigned>(tgt - col0) < static_cast<unsigned>(kCols) && tgt < a.vocab) {
+        if (tgt >= 0 && static_cast<unsigned>(tgt - col0) < static_cast<unsigned>(kCols)) {
           float z = 0.f;
 #pragma unroll
           for (int c = 0; c < kCols / 32; ++c)
@@ -438,20 +448,13 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           if (row < a.M) a.part[static_cast<int64_t>(2 * w.n + half) * a.part_ld + row] = now;
         } else {
           run_mx = now.x, run_sum = now.y;
-          if (t + workers >= ntiles && row < a.M) a.part[static_cast<int64_t>(2 * worker + half) * a.part_ld + row] = now;
+          if (q + 1 == mine && row < a.M) a.part[static_cast<int64_t>(2 * worker + half) * a.part_ld + row] = now;
         }
       } else {
         if (!ready()) break;
         const uint32_t tm = tm0 + (local % kBufs) * kN;
         if constexpr (MODE == kVgGrad) {
-          int tgt = -1;
-          float l2 = 0.f, gi = 0.f;
-          if (row < a.M) {
-            tgt = a.targets.get(row);
-            if (tgt >= a.vocab) tgt = -1;
-            l2 = a.lse[row] * kLog2e;
-            gi = a.dloss[row] / s;
-          }
+          const float l2 = row_lse * kLog2e, gi = row_dloss / s;
           const int rel = tgt - a.v0;   // column of the target in this piece (maybe outside)
 #pragma unroll 1
           for (int c = 0; c < kCols / 64; ++c) {
@@ -591,25 +594,23 @@ __global__ void __launch_bounds__(512) vocab_loss_kernel(const float2* part, int
   loss[i] = held ? l - z : 0.f;
 }
 
-// dh = s * the sum of the splits, in order
+// dh = s * the sum of the splits, in order; four values a thread, sixteen splits requested together
 template <typename To>
 __global__ void __launch_bounds__(256) vocab_hidden_kernel(const float* part, int splits, int64_t n, const float* scale,
                                                            To* dh) {
   pdl_wait();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i >= n) return;
   const float s = scale[0];
-  float f[8] = {};
-#pragma unroll 8
+  float f[4] = {};
+#pragma unroll 16
   for (int k = 0; k < splits; ++k) {
-    float p[8];
-    load8_rw(part + k * n + i, p);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] += p[j];
+    const float4 p = *reinterpret_cast<const float4*>(part + k * n + i);
+    f[0] += p.x, f[1] += p.y, f[2] += p.z, f[3] += p.w;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] *= s;
-  store8(dh + i, f);
+  for (int j = 0; j < 4; ++j) f[j] *= s;
+  store4(dh + i, f);
 }
 
 }  // namespace dm0
