@@ -28,6 +28,16 @@ def eng():
     e.close()
 
 
+@pytest.fixture(autouse=True)
+def unwritten_memory_is_nan():
+    """Fills what torch's allocator will hand out next with NaN, so that a value that a kernel left out shows."""
+    held = [torch.full((n,), float("nan"), device="cuda") for n in [2 ** k for k in range(7, 18)] * 24 + [2 ** 22] * 8
+            + [2 ** 26] * 2]
+    torch.cuda.synchronize()
+    del held
+    yield
+
+
 def rng(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 

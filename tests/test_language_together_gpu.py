@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from synth import inputs as I
-from tests.test_language_gpu import BF, BF16, F32, eng, ids_of, loss_case, norm_case, randn, rng  # noqa: F401
+from tests.test_language_gpu import (BF, BF16, F32, eng, ids_of, loss_case, norm_case, randn, rng,  # noqa: F401
+                                     unwritten_memory_is_nan)
 
 pytestmark = pytest.mark.gpu
 

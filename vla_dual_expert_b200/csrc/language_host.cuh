@@ -393,7 +393,7 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   }
   if (!dh) return DM0_OK;
   const int64_t n = static_cast<int64_t>(tokens) * H;
-  const dim3 grid(static_cast<unsigned>((n / 8 + 255) / 256));
+  const dim3 grid(static_cast<unsigned>((n / 4 + 255) / 256));
   // the splits of the first piece; the last piece may have used fewer
   const int splits = p.splits;
   if (dh_f32)

@@ -75,32 +75,38 @@ struct VgTile {
   static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
-// 32 rows x 64 bf16 (values of one lane: its row's 64 columns) through the warp's scratch, to rows of
-// `dst` that are `ld` elements apart; 4 whole 128-byte row pieces per store instruction
-__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&lo)[32], const float (&hi)[32],
-                                              __nv_bfloat16* dst, int64_t ld, int rows) {
-  const int lane = threadIdx.x & 31;
+// 32 rows x 64 bf16 (values of one lane: its row's 64 columns) through the warp's 4 KB of scratch, to rows of
+// `dst` that are `ld` elements apart; 4 whole 128-byte row pieces per store instruction.  The tiles of few
+// tokens are all epilogue, two warps to a scheduler, so its instructions count: addresses by one exclusive or or an
+// immediate, paired multiplications, one accumulator load per chunk.
+__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&v)[64], __nv_bfloat16* dst, int64_t ld,
+                                              int rows) {
+  const int lane = threadIdx.x & 31, qr = lane >> 3, qc = lane & 7;
+  const uint32_t w = smem_u32(scr) + lane * 128 + ((lane & 7) << 4);   // scr is 1024-byte aligned
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    *reinterpret_cast<uint4*>(scr + resid_swz(lane, j)) =
-        make_uint4(bf2(lo[8 * j], lo[8 * j + 1]), bf2(lo[8 * j + 2], lo[8 * j + 3]), bf2(lo[8 * j + 4], lo[8 * j + 5]),
-                   bf2(lo[8 * j + 6], lo[8 * j + 7]));
-    *reinterpret_cast<uint4*>(scr + resid_swz(lane, j + 4)) =
-        make_uint4(bf2(hi[8 * j], hi[8 * j + 1]), bf2(hi[8 * j + 2], hi[8 * j + 3]), bf2(hi[8 * j + 4], hi[8 * j + 5]),
-                   bf2(hi[8 * j + 6], hi[8 * j + 7]));
-  }
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(w ^ (j << 4)), "r"(bf2(v[8 * j], v[8 * j + 1])),
+                 "r"(bf2(v[8 * j + 2], v[8 * j + 3])), "r"(bf2(v[8 * j + 4], v[8 * j + 5])),
+                 "r"(bf2(v[8 * j + 6], v[8 * j + 7]))
+                 : "memory");
   __syncwarp();
-  const int qr = lane >> 3, qc = lane & 7;
+  const uint8_t* even = scr + qr * 128 + ((qc ^ qr) << 4);              // rows 8 k + qr
+  const uint8_t* odd = scr + (qr + 4) * 128 + ((qc ^ (qr + 4)) << 4);   // rows 8 k + 4 + qr
+  __nv_bfloat16* d = dst + qr * ld + qc * 8;
+  if (rows >= 32) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + qr;
-    if (r < rows)
-      *reinterpret_cast<uint4*>(dst + r * ld + qc * 8) = *reinterpret_cast<const uint4*>(scr + resid_swz(r, qc));
+    for (int i = 0; i < 8; ++i, d += 4 * ld)
+      *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>((i & 1 ? odd : even) + (i >> 1) * 1024);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i, d += 4 * ld)
+      if (4 * i + qr < rows)
+        *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>((i & 1 ? odd : even) + (i >> 1) * 1024);
   }
   __syncwarp();
 }
 // 32 rows x 32 fp32, added to what is there if `add`
-__device__ __forceinline__ void vg_store_f32(uint8_t* scr, const float (&v)[32], float* dst, int64_t ld, int rows,
+__device__ __forceinline__ void vg_store_f32(uint8_t* scr, const float* v, float* dst, int64_t ld, int rows,
                                              bool add) {
   const int lane = threadIdx.x & 31;
   const int qr = lane >> 3, qc = lane & 7;
@@ -438,12 +444,15 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
         }
         mx = fmaxf(mx, run_mx);
         const float ref = mx == -INFINITY ? 0.f : mx * kLog2e;
-        float sum[4] = {run_sum * ex2_fast(run_mx * kLog2e - ref), 0.f, 0.f, 0.f};
+        float2 sum[2] = {make_float2(run_sum * ex2_fast(run_mx * kLog2e - ref), 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sum[j & 3] += ex2_fast(fmaf(v[c][j], kLog2e, -ref));
-        const float2 now = make_float2(mx, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+          for (int j = 0; j < 32; j += 2) {
+            const float2 x = ffma2(make_float2(v[c][j], v[c][j + 1]), make_float2(kLog2e, kLog2e), make_float2(-ref, -ref));
+            sum[(j >> 1) & 1] = fadd2(sum[(j >> 1) & 1], make_float2(ex2_fast(x.x), ex2_fast(x.y)));
+          }
+        const float2 now = make_float2(mx, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         if (a.mt > 1) {
           if (row < a.M) a.part[static_cast<int64_t>(2 * w.n + half) * a.part_ld + row] = now;
         } else {
@@ -458,26 +467,27 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           const int rel = tgt - a.v0;   // column of the target in this piece (maybe outside)
 #pragma unroll 1
           for (int c = 0; c < kCols / 64; ++c) {
-            float v[2][32];
+            float v[64];
+            tmem_ld64(tm + 64 * c, v);
+            if (c + 1 == kCols / 64) release();
+            const int cc = col0 + 64 * c;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              tmem_ld32(tm + 64 * c + 32 * q, v[q]);
-              if (c + 1 == kCols / 64 && q == 1) release();
-              const int cc = col0 + 64 * c + 32 * q;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[q][j] = ex2_fast(fmaf(v[q][j], kLog2e, -l2)) * gi;
-              if (static_cast<unsigned>(rel - cc) < 32u) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (rel - cc == j) v[q][j] -= gi;
-              }
-              if (tgt < 0 || cc + 32 > a.valid_n) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (tgt < 0 || cc + j >= a.valid_n) v[q][j] = 0.f;
-              }
+            for (int j = 0; j < 64; j += 2) {
+              const float2 x = ffma2(make_float2(v[j], v[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-l2, -l2));
+              const float2 p = fmul2(make_float2(ex2_fast(x.x), ex2_fast(x.y)), make_float2(gi, gi));
+              v[j] = p.x, v[j + 1] = p.y;
             }
-            vg_store_bf16(scr, v[0], v[1], a.g + static_cast<int64_t>(row0) * a.ldg + col0 + 64 * c, a.ldg, rows);
+            if (static_cast<unsigned>(rel - cc) < 64u) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (rel - cc == j) v[j] -= gi;
+            }
+            if (tgt < 0 || cc + 64 > a.valid_n) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (tgt < 0 || cc + j >= a.valid_n) v[j] = 0.f;
+            }
+            vg_store_bf16(scr, v, a.g + static_cast<int64_t>(row0) * a.ldg + cc, a.ldg, rows);
           }
         } else if (!w.second) {
           float* dst = a.dh + (static_cast<int64_t>(w.split) * a.M + row0) * a.N + col0;
@@ -492,21 +502,21 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           const int64_t at = static_cast<int64_t>(a.v0 + row0) * a.N + col0;
 #pragma unroll 1
           for (int c = 0; c < kCols / 64; ++c) {
-            float v[2][32];
-            tmem_ld32(tm + 64 * c, v[0]);
-            tmem_ld32(tm + 64 * c + 32, v[1]);
+            float v[64];
+            tmem_ld64(tm + 64 * c, v);
             if (c + 1 == kCols / 64) release();
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[q][j] *= s;
+            for (int j = 0; j < 64; j += 2) {
+              const float2 x = fmul2(make_float2(v[j], v[j + 1]), make_float2(s, s));
+              v[j] = x.x, v[j + 1] = x.y;
+            }
             if (col0 + 64 * c >= a.N) continue;
             if (a.dw_f32) {
               float* dst = static_cast<float*>(a.dw) + at + 64 * c;
-              vg_store_f32(scr, v[0], dst, a.N, rows, a.add != 0);
-              vg_store_f32(scr, v[1], dst + 32, a.N, rows, a.add != 0);
+              vg_store_f32(scr, v, dst, a.N, rows, a.add != 0);
+              vg_store_f32(scr, v + 32, dst + 32, a.N, rows, a.add != 0);
             } else {
-              vg_store_bf16(scr, v[0], v[1], static_cast<__nv_bfloat16*>(a.dw) + at + 64 * c, a.N, rows);
+              vg_store_bf16(scr, v, static_cast<__nv_bfloat16*>(a.dw) + at + 64 * c, a.N, rows);
             }
           }
         }
