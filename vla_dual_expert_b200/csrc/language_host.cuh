@@ -201,6 +201,18 @@ dm0_status vg_tmap(dm0_ctx* c, CUtensorMap* m, const void* p, uint64_t rows, uin
   return r == CUDA_SUCCESS ? DM0_OK : fail(c, DM0_ECUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
 }
 
+// G's map: [panels][tokens][64] bf16, boxes of one panel's `box` tokens
+dm0_status vg_panel_tmap(dm0_ctx* c, CUtensorMap* m, const void* p, uint64_t tokens, uint64_t panels, uint32_t box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(c, DM0_ECUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {64, tokens, panels}, strides[2] = {128, 128 * tokens};
+  cuuint32_t boxd[3] = {64, box, 1}, estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, boxd, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DM0_OK : fail(c, DM0_ECUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
+}
+
 // More than 128 tokens: pairs of CTAs on 256 x 256 tiles; up to 128: one CTA on 128 x 128, where a pair's
 // second half of the rows would be padding.
 bool vocab_pairs(int tokens) { return tokens > 128; }
@@ -290,7 +302,7 @@ dm0_status vocab_gemm(dm0_ctx* c, cudaStream_t s, bool pairs, const dm0::VgMaps&
 dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16* w, dm0::Ids tgt, int tokens, int vocab,
                           int H, float* loss, float* lse, uint8_t* ws) {
   const VocabLossPlan p = vocab_loss_plan(tokens, vocab);
-  dm0::VgMaps m;
+  dm0::VgMaps m{};
   const bool pairs = vocab_pairs(tokens);
   TRY(vg_tmap(c, &m.a, h, tokens, H, vocab_a_rows(tokens)));
   TRY(vg_tmap(c, &m.b, w, vocab, H, 128));
@@ -328,13 +340,15 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   float* part = reinterpret_cast<float*>(ws + p.dh);
   const bool pairs = vocab_pairs(tokens);
   const int tile = vocab_tile(tokens);
-  dm0::VgMaps mg, mh, mw;   // operands of G, dh and dW
+  dm0::VgMaps mg{}, mh{}, mw{};   // of G, dh and dW
   TRY(vg_tmap(c, &mg.a, h, tokens, H, vocab_a_rows(tokens)));
   TRY(vg_tmap(c, &mg.b, w, vocab, H, 128));
-  TRY(vg_tmap(c, &mh.a, g, tokens, p.piece, vocab_a_rows(tokens)));
+  TRY(vg_panel_tmap(c, &mg.out, g, tokens, p.piece / 64, 32));
+  if (dw && !dw_f32) TRY(vg_tmap(c, &mw.out, dw, vocab, H, 32));
+  TRY(vg_panel_tmap(c, &mh.a, g, tokens, p.piece / 64, vocab_a_rows(tokens)));
   TRY(vg_tmap(c, &mh.b, w, vocab, H, 64));
   const int kbox = std::min(64, (tokens + 15) / 16 * 16);   // tokens of a k-block of dW
-  TRY(vg_tmap(c, &mw.a, g, tokens, p.piece, kbox));
+  TRY(vg_panel_tmap(c, &mw.a, g, tokens, p.piece / 64, kbox));
   TRY(vg_tmap(c, &mw.b, h, tokens, H, kbox));
   const int mt = (tokens + tile - 1) / tile, ht = (H + tile - 1) / tile;
   for (int v0 = 0; v0 < vocab; v0 += p.piece) {
@@ -359,8 +373,6 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
     a.valid_n = cols;
     a.lse = lse;
     a.dloss = dloss;
-    a.g = g;
-    a.ldg = p.piece;
     TRY(vocab_gemm<dm0::kVgGrad>(c, s, pairs, mg, a));
     dm0::VgArgs ah = a, aw = a;
     ah.N = H;
@@ -382,8 +394,7 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
     aw.band = 1;
     aw.b_y0 = 0;
     aw.add = accumulate;
-    aw.dw = dw;
-    aw.dw_f32 = dw_f32;
+    aw.dw = dw_f32 ? static_cast<float*>(dw) : nullptr;
     dim3 grid;
     TRY(vocab_grid(c, pairs, vocab_tiles(ah) + vocab_tiles(aw), &grid));
     if (pairs)

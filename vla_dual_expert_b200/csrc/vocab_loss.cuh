@@ -16,6 +16,10 @@
 // (a constant dloss that is no power of two would otherwise put one and the same relative error of up to
 // 2^-8 / 2 into every entry -dloss of the targets, which no sum averages out).
 //
+// G lies in panels of 64 columns, [panel][token][64], so that every box of it, 64 columns x some tokens, is one
+// stretch of memory; as [token][column] a box's rows lay 2 x piece bytes apart, a
+// power of two (both gradients of 256 tokens x 131072 x 2048: 505 -> 490 us).
+//
 // The products are bound by the tensor cores for many tokens and by one read of W for few.
 #pragma once
 #include "attention_tc.cuh"   // sw128_mnmajor_desc
@@ -49,13 +53,10 @@ struct VgArgs {
   float* zt;            // [tokens] logit of the target
   const float *lse, *dloss;
   float* scale;         // scale[0] = s: found by the first piece's kVgGrad, read by the others
-  __nv_bfloat16* g;     // [tokens][ldg]
-  int ldg;
   // dh: fp32 sums of the splits, [split][tokens][H]; dW: rows of the piece
   float* dh;
   int add;              // add to what is there (dh: from the second piece on; dW: accumulate)
-  void* dw;             // [vocab][H]
-  int dw_f32;
+  float* dw;            // [vocab][H] in fp32; null: bf16 through the map
 };
 
 // Tile of a CTA pair (cta_group::2): 256 rows of A times 256 rows of B, of which each CTA stages half.  Tile of
@@ -75,13 +76,35 @@ struct VgTile {
   static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
-// 32 rows x 64 bf16 (values of one lane: its row's 64 columns) through the warp's 4 KB of scratch, to rows of
-// `dst` that are `ld` elements apart; 4 whole 128-byte row pieces per store instruction.  The tiles of few
-// tokens are all epilogue, two warps to a scheduler, so its instructions count: addresses by one exclusive or or an
-// immediate, paired multiplications, one accumulator load per chunk.
-__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&v)[64], __nv_bfloat16* dst, int64_t ld,
+// Copy of a box from shared memory to a tensor (rows and columns outside it are not written), its group, and the
+// waits for the groups' reads and for their writes; by one lane of a warp.
+__device__ __forceinline__ void vg_copy_out(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void vg_copy_out_panel(const CUtensorMap* map, const void* src, int row, int panel) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(0), "r"(row), "r"(panel)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void vg_scratch_free() {
+  if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+// 32 rows x 64 bf16 (values of one lane: its row's 64 columns) through the warp's 4 KB of scratch, in the layout of
+// a 128-byte-swizzled box, and from there by one copy.  The tiles of few tokens are all epilogue, two warps to a
+// scheduler, so its instructions count: addresses by one exclusive or, paired multiplications, one accumulator load
+// per chunk, and no loads and stores of the rows by the warp.
+template <bool PANEL>
+__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&v)[64], const CUtensorMap* map, int x, int y,
                                               int rows) {
-  const int lane = threadIdx.x & 31, qr = lane >> 3, qc = lane & 7;
+  const int lane = threadIdx.x & 31;
+  vg_scratch_free();
   const uint32_t w = smem_u32(scr) + lane * 128 + ((lane & 7) << 4);   // scr is 1024-byte aligned
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -89,21 +112,14 @@ __device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&v)[64]
                  "r"(bf2(v[8 * j + 2], v[8 * j + 3])), "r"(bf2(v[8 * j + 4], v[8 * j + 5])),
                  "r"(bf2(v[8 * j + 6], v[8 * j + 7]))
                  : "memory");
+  fence_async_smem();
   __syncwarp();
-  const uint8_t* even = scr + qr * 128 + ((qc ^ qr) << 4);              // rows 8 k + qr
-  const uint8_t* odd = scr + (qr + 4) * 128 + ((qc ^ (qr + 4)) << 4);   // rows 8 k + 4 + qr
-  __nv_bfloat16* d = dst + qr * ld + qc * 8;
-  if (rows >= 32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i, d += 4 * ld)
-      *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>((i & 1 ? odd : even) + (i >> 1) * 1024);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i, d += 4 * ld)
-      if (4 * i + qr < rows)
-        *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>((i & 1 ? odd : even) + (i >> 1) * 1024);
+  if (lane == 0 && rows > 0) {
+    if (PANEL)
+      vg_copy_out_panel(map, scr, y, x >> 6);
+    else
+      vg_copy_out(map, scr, x, y);
   }
-  __syncwarp();
 }
 // 32 rows x 32 fp32, added to what is there if `add`
 __device__ __forceinline__ void vg_store_f32(uint8_t* scr, const float* v, float* dst, int64_t ld, int rows,
@@ -146,7 +162,7 @@ constexpr int kVgStretch = 8;
 // CTAs' stages and fill both accumulators, and both epilogues free its `tempty`.
 // kVgBack's tiles: dh's first, then dW's, each product with its own operands.
 struct VgMaps {
-  CUtensorMap a, b;
+  CUtensorMap a, b, out;   // operands, and a bf16 result: boxes of 64 columns x 32 rows
 };
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, const VgMaps& m1, const VgArgs& a1) {
@@ -253,9 +269,17 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
             else
               tma_load_2d(dst, &map, &full[s], x, y, keep);
           };
+          auto load_panel = [&](uint8_t* dst, int row, int panel) {   // of G
+            if constexpr (PAIR)
+              tma_load_3d_pair(dst, &maps.a, bar, 0, row, panel, keep);
+            else
+              tma_load_3d(dst, &maps.a, &full[s], 0, row, panel, keep);
+          };
           if (a_mn) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) load(sa + 8192 * j, maps.a, ra + 64 * j, kb * 64);
+            for (int j = 0; j < 2; ++j) load_panel(sa + 8192 * j, kb * 64, (ra >> 6) + j);
+          } else if (MODE == kVgBack) {
+            load_panel(sa, ra, kb);
           } else {
             load(sa, maps.a, kb * 64, ra);
           }
@@ -487,9 +511,10 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
               for (int j = 0; j < 64; ++j)
                 if (tgt < 0 || cc + j >= a.valid_n) v[j] = 0.f;
             }
-            vg_store_bf16(scr, v, a.g + static_cast<int64_t>(row0) * a.ldg + cc, a.ldg, rows);
+            vg_store_bf16<true>(scr, v, &m0.out, cc, row0, rows);
           }
         } else if (!w.second) {
+          vg_scratch_free();
           float* dst = a.dh + (static_cast<int64_t>(w.split) * a.M + row0) * a.N + col0;
 #pragma unroll 1
           for (int c = 0; c < kCols / 32; ++c) {
@@ -511,17 +536,18 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
               v[j] = x.x, v[j + 1] = x.y;
             }
             if (col0 + 64 * c >= a.N) continue;
-            if (a.dw_f32) {
-              float* dst = static_cast<float*>(a.dw) + at + 64 * c;
+            if (a.dw) {
+              float* dst = a.dw + at + 64 * c;
               vg_store_f32(scr, v, dst, a.N, rows, a.add != 0);
               vg_store_f32(scr, v + 32, dst + 32, a.N, rows, a.add != 0);
             } else {
-              vg_store_bf16(scr, v, static_cast<__nv_bfloat16*>(a.dw) + at + 64 * c, a.N, rows);
+              vg_store_bf16<false>(scr, v, &m1.out, col0 + 64 * c, a.v0 + row0, rows);
             }
           }
         }
       }
     }
+    if (MODE != kVgStats && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // results written
   }
   tc_fence_before();
   __syncthreads();
