@@ -74,7 +74,8 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// One warp per row; a lane's 16-byte pieces of the row are requested together.  Bound by HBM.
+// One warp per row; a lane's 16-byte pieces of the row are requested together.  Bound by HBM: 32768 rows of 2048 in
+// 38 us, 7.0 TB/s of rows read and written (some of the frequent rows come from L2); one row by the launch, 4 us.
 template <typename To>
 __global__ void __launch_bounds__(256) embed_kernel(const __nv_bfloat16* table, Ids ids, int n, int vocab, int H,
                                                     float scale, To* out, RowsView ov, int* err) {
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(256) embed_kernel(const __nv_bfloat16* table, 
 constexpr int kEmbTile = 32;        // sorted positions per tile of the sums; a longer segment is cut at tiles
 constexpr int kSortWarps = 16;
 constexpr int kSortMaxRows = 1600;  // vocabulary rows of one sorting CTA: 16 warps x 1600 counters = 100 KB
+constexpr int kSortList = 512;      // of its own ids, that a warp keeps between the passes
 constexpr int kSortZero = 1 << 16;  // bytes that one of the sort's zeroing CTAs writes
 
 // Scratch of one gradient.  Sorted place i holds position perm[i] of id row_of[i]; seg[v] is the range of
@@ -123,17 +125,18 @@ struct EmbScratch {
 
 // Each of G CTAs (a power of two) owns the ids v with v mod G = its index, so that neighbouring frequent ids
 // fall to different CTAs.  Each reads every id: it counts those of smaller owners (its place in the sorted list,
-// so the CTAs need no exchange) and its own per (warp, row), warp w taking the w-th stretch of positions;
-// after a scan it writes the positions in (row, position) order.  The ids come from L2: G x n x 8 bytes,
-// twice.  A lane's rank among equal ids of its 32 is counted over the lanes that hold ids of this CTA, few
-// as a rule; match.any in its place took 10 us longer (32768 tokens, 6% of them one id).
+// so the CTAs need no exchange) and its own per (warp, row), warp w taking the w-th stretch of positions and
+// listing its own; after a scan it writes the listed positions in (row, position) order (a warp with more than
+// kSortList of them reads its stretch again).  The ids come from L2, G times.  An entry's rank among equal ids of
+// its 32 is counted over the lanes.  32768 tokens x 131072 rows, 6% of the tokens one id: 25 us; 37 with every id
+// read and tested in both passes, and match.any for the ranks took 10 us more.
 // The sort leaves HBM idle, so the CTAs behind the first G write zeros meanwhile: `zero_bytes` of the gradient
 // from `zero`, the rows of the highest ids, whether their ids occur or not (the sums come later).
 template <typename Id>
 __global__ void __launch_bounds__(kSortWarps * 32, 2) embed_sort_kernel(const Id* ids, int n, int vocab, int log_g, int rows,
                                                                         EmbScratch o, uint8_t* zero,
                                                                         int64_t zero_bytes, int* err) {
-  extern __shared__ int cnt[];   // [kSortWarps][rows]
+  extern __shared__ int cnt[];   // [kSortWarps][rows], then the lists
   __shared__ int warp_tot[kSortWarps], below_tot[kSortWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int own = blockIdx.x, mask = (1 << log_g) - 1;
@@ -154,10 +157,10 @@ __global__ void __launch_bounds__(kSortWarps * 32, 2) embed_sort_kernel(const Id
   const int stretch = (warp + own) % kSortWarps;
   const int p0 = min(n, stretch * chunk), p1 = min(n, p0 + chunk);
   int* mine = cnt + stretch * rows;
-  int below = 0;
+  int* list = cnt + kSortWarps * rows + warp * kSortList;   // this warp's own ids: place in the stretch, row (11 bits)
+  int below = 0, listed = 0;
   bool bad = false;
-  // 1024 positions of a warp at a time, all requested together; with up to 16384 tokens one round serves both
-  // passes.  -1: not a token
+  // 1024 positions of a warp at a time, sixteen requested together.  -1: not a token
   constexpr int U = 32;
   int id[U];
   auto fetch = [&](int b) {
@@ -184,7 +187,14 @@ __global__ void __launch_bounds__(kSortWarps * 32, 2) embed_sort_kernel(const Id
       if (b + 32 * u >= p1) break;
       const int k = id[u] & mask;
       if (id[u] >= 0) below += k < own;
-      if (id[u] >= 0 && k == own) atomicAdd(&mine[id[u] >> log_g], 1);
+      const bool in = id[u] >= 0 && k == own;
+      const unsigned act = __ballot_sync(0xffffffffu, in);
+      if (!act) continue;
+      const int at = listed + __popc(act & ((1u << lane) - 1u));
+      listed += __popc(act);
+      if (!in) continue;
+      atomicAdd(&mine[id[u] >> log_g], 1);
+      if (at < kSortList) list[at] = ((b + 32 * u + lane - p0) << 11) | (id[u] >> log_g);
     }
   }
   if (bad && blockIdx.x == 0) raise_error(err, kErrBounds);
@@ -233,29 +243,39 @@ __global__ void __launch_bounds__(kSortWarps * 32, 2) embed_sort_kernel(const Id
   }
   if (tid == 0 && own == mask) o.total[0] = carry;
   if (carry == base) return;   // none of its ids occurs
-  for (int b = p0; b < p1; b += 32 * U) {
-    if (p1 - p0 > 32 * U) fetch(b);
+  // places within a row, 32 entries of the stretch at a time
+  auto place = [&](bool in, int bin, int position) {
+    int rank = 0, same = 0;
+    for (unsigned rest = __ballot_sync(0xffffffffu, in); rest; rest &= rest - 1) {
+      const int l = __ffs(rest) - 1;
+      const bool eq = __shfl_sync(0xffffffffu, bin, l) == bin;
+      same += eq;
+      rank += eq && l < lane;
+    }
+    if (in) {
+      const int at = mine[bin] + rank;
+      o.perm[at] = position;
+      o.row_of[at] = (bin << log_g) + own;
+    }
+    __syncwarp();
+    if (in && rank == 0) mine[bin] += same;
+    __syncwarp();
+  };
+  if (listed <= kSortList) {
+    for (int b = 0; b < listed; b += 32) {
+      const bool in = b + lane < listed;
+      const int e = in ? list[b + lane] : 0;
+      place(in, in ? e & 2047 : -1, p0 + (e >> 11));
+    }
+    return;
+  }
+  for (int b = p0; b < p1; b += 32 * U) {   // too many for the list: the ids once more
+    fetch(b);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (b + 32 * u >= p1) break;
       const bool in = id[u] >= 0 && (id[u] & mask) == own;
-      unsigned act = __ballot_sync(0xffffffffu, in);
-      if (!act) continue;
-      int rank = 0, same = 0;
-      for (unsigned rest = act; rest; rest &= rest - 1) {
-        const int l = __ffs(rest) - 1;
-        const bool eq = __shfl_sync(0xffffffffu, id[u], l) == id[u];
-        same += eq;
-        rank += eq && l < lane;
-      }
-      if (in) {
-        const int at = mine[id[u] >> log_g] + rank;
-        o.perm[at] = b + 32 * u + lane;
-        o.row_of[at] = id[u];
-      }
-      __syncwarp();
-      if (in && rank == 0) mine[id[u] >> log_g] += same;
-      __syncwarp();
+      if (__ballot_sync(0xffffffffu, in)) place(in, in ? id[u] >> log_g : -1, b + 32 * u + lane);
     }
   }
 }
@@ -283,6 +303,8 @@ struct Raw8<float> {
 // walking the tile's rows, eight requested ahead.  A segment of up to kEmbTile places belongs whole to the tile
 // where it begins (at most 63 rows a tile); a longer one is cut at the tiles and leaves partial sums.  The
 // other blocks write the zero rows of ids below zero_rows that never occur (none when the gradient is added to).
+// Bound by HBM: 32768 tokens of 2048 in bf16 into 131072 fp32 rows, 154 us for 0.93 GB at 6.0 TB/s (215 us with the
+// zeroing blocks behind the summing ones and tiles of 64 places at half the blocks per SM).
 constexpr int kEmbCols = 2048;   // columns of one block: 256 threads x 8
 constexpr int kEmbZeroRows = 16;
 template <typename Td>

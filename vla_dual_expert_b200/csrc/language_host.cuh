@@ -73,15 +73,15 @@ dm0_status embed_grad_run(dm0_ctx* c, cudaStream_t s, dm0::Ids ids, int n, const
     return ids.wide ? few(dm0::embed_few_kernel<long long, Td>, static_cast<const long long*>(ids.p))
                     : few(dm0::embed_few_kernel<int, Td>, static_cast<const int*>(ids.p));
   }
-  // rows that the sort's shadow has time to zero: about 6 us and 1.2 ns a token, at 5 TB/s
-  const double shadow = (6e-6 + 1.2e-9 * n) * 5e12;
+  // rows that the sort's shadow has time to zero: about 3 us and 1.6 ns a token, at 5 TB/s
+  const double shadow = (3e-6 + 1.6e-9 * n) * 5e12;
   const int early = accumulate ? 0 : static_cast<int>(std::min<double>(vocab, shadow / (4.0 * H)));
   const int64_t zero_bytes = 4ll * H * early;
   const int zero_rows = accumulate ? 0 : vocab - early;
   auto sort = [&](auto kernel, auto typed) {
     return launch(c, s, kernel,
                   dim3((1 << p.log_g) + static_cast<unsigned>((zero_bytes + dm0::kSortZero - 1) / dm0::kSortZero)),
-                  dim3(dm0::kSortWarps * 32), sizeof(int) * dm0::kSortWarps * p.rows, typed, n, vocab, p.log_g, p.rows,
+                  dim3(dm0::kSortWarps * 32), sizeof(int) * dm0::kSortWarps * (p.rows + dm0::kSortList), typed, n, vocab, p.log_g, p.rows,
                   o, reinterpret_cast<uint8_t*>(grad + static_cast<int64_t>(zero_rows) * H), zero_bytes, c->d_err);
   };
   TRY(ids.wide ? sort(dm0::embed_sort_kernel<long long>, static_cast<const long long*>(ids.p))
@@ -423,8 +423,8 @@ bool lang_setup() {
   return norm_grad_setup<f, f, f>() && norm_grad_setup<f, f, bf16>() && norm_grad_setup<f, bf16, f>() &&
          norm_grad_setup<f, bf16, bf16>() && norm_grad_setup<bf16, f, f>() && norm_grad_setup<bf16, f, bf16>() &&
          norm_grad_setup<bf16, bf16, f>() && norm_grad_setup<bf16, bf16, bf16>() &&
-         attr(dm0::embed_sort_kernel<int>, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
-         attr(dm0::embed_sort_kernel<long long>, 4 * dm0::kSortWarps * dm0::kSortMaxRows) &&
+         attr(dm0::embed_sort_kernel<int>, 4 * dm0::kSortWarps * (dm0::kSortMaxRows + dm0::kSortList)) &&
+         attr(dm0::embed_sort_kernel<long long>, 4 * dm0::kSortWarps * (dm0::kSortMaxRows + dm0::kSortList)) &&
          attr(dm0::vocab_gemm_kernel<dm0::kVgStats>, dm0::VgTile<false>::kBytes) &&
          attr(dm0::vocab_gemm_kernel<dm0::kVgGrad>, dm0::VgTile<false>::kBytes) &&
          attr(dm0::vocab_back_kernel, dm0::VgTile<false>::kBytes) &&

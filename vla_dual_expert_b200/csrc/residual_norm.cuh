@@ -51,7 +51,8 @@ __device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
 }
 
 // Forward: W warps per row, 16 values per thread in registers between the two norms.  Small blocks, so that
-// many are resident and one row's loads overlap another's reductions and stores.
+// many are resident and one row's loads overlap another's reductions and stores: 32768 x 2048 (fp32 h, bf16 y) in
+// 124 us, 6.5 TB/s (264 us with a warp per row and 64 values a lane: one block per SM, loads and stores by turns).
 template <typename Th, typename Ty, int W>
 __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) residual_norm_kernel(const Th* h, const Ty* y, RnArgs a,
                                                                             Th* h_out, __nv_bfloat16* n_out,
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) residual_norm_kernel(con
 // Backward over a stripe of one sample's rows: a thread owns 8 columns and keeps their sums A, B, C; the
 // row's three sums (of a dn x, of w z (dh' + r a dn), of w z x, from which both means follow) take one block
 // reduction.  The rows come by bulk copies into a ring of `stages` rows in shared memory, so the reads of
-// later rows go on through a row's reduction and stores.
+// later rows go on through a row's reduction and stores: 32768 x 2048 in 189 us at 6.2 TB/s and 10 us for the sums
+// of the stripes (276 us in all with loads into registers, a row at a time).
 //   part[stripe][3][H]: the stripe's A, B, C.
 constexpr int kRnMaxStages = 4;
 struct RnGradArgs {

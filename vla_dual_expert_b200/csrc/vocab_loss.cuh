@@ -20,7 +20,12 @@
 // stretch of memory; as [token][column] a box's rows lay 2 x piece bytes apart, a
 // power of two (both gradients of 256 tokens x 131072 x 2048: 505 -> 490 us).
 //
-// The products are bound by the tensor cores for many tokens and by one read of W for few.
+// The products are bound by the tensor cores for many tokens, under load by the power limit: the loss of 4096
+// tokens x 131072 x 2048 takes 1.67 ms one after another, 1320 TFLOP/s (the library's bf16 product that writes those
+// logits 1.74 ms), the gradients of 8192 tokens 10.5 ms, 1260 TFLOP/s (the library's three products 10.0 ms).  With
+// few tokens they are bound by HBM: the loss reads W once (7 tokens: 91 us alone, 103 among calls with other
+// weights, 82 at the rate of a copy); the gradient twice, as its second product needs G's whole rows, and dW is
+// written (316 us, 245 at that rate).
 #pragma once
 #include "attention_tc.cuh"   // sw128_mnmajor_desc
 #include "embedding.cuh"
