@@ -473,8 +473,8 @@ dm0_status dm0_vocab_loss(dm0_ctx* ctx, const void* hidden_states, const void* w
 size_t dm0_vocab_loss_workspace(int tokens, int vocab, int hidden);
 
 /* Gradient of sum_i dloss[i] loss[i] from the lse of dm0_vocab_loss (dloss: device f32 [tokens], not read into the
- * result where there is no target).  With G = (softmax - onehot) dloss, divided by the largest |dloss| and rounded to
- * bf16 as the products' operand:
+ * result where there is no target).  With G = (softmax - onehot) dloss, divided by the largest finite |dloss| and
+ * rounded to bf16 as the products' operand:
  *   dhidden = G weight:          device fp32 or bf16 [tokens][hidden], or null
  *   dweight = G^T hidden_states: device fp32 or bf16 [vocab][hidden], or null; accumulate != 0 (fp32 only) adds to it
  * The logits are built again, in pieces of the vocabulary of at most 2^27 entries (256 MB of the workspace). */

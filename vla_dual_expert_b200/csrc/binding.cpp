@@ -164,10 +164,11 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& body) {
 }
 template <class F>
 dm0_status without_gil(F&& call) {
-  PyThreadState* save = PyEval_SaveThread();
-  const dm0_status st = call();
-  PyEval_RestoreThread(save);
-  return st;
+  struct Released {
+    PyThreadState* save = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(save); }
+  } released;
+  return call();
 }
 
 struct IdList {

@@ -11,14 +11,14 @@
 //             dh += G W:  A = G (K-major), B = W read along H (MN-major), fp32 sums
 //             dW = G^T h: A = G read along V (MN-major), B = h read along H (MN-major)
 //
-// s = max |dloss_i|, of the finite ones of the tokens with a target: G / s is what is rounded to bf16 and s multiplies the
-// fp32 results, so the factor 1 / tokens of a mean, the same in every row, takes no part in the rounding
-// (a constant dloss that is no power of two would otherwise put one and the same relative error of up to
-// 2^-8 / 2 into every entry -dloss of the targets, which no sum averages out).
+// s = max |dloss_i|, of the finite ones of the tokens with a target: G / s is what is rounded to bf16 (half a step:
+// 2^-8 of the value) and s multiplies the fp32 results, so the factor 1 / tokens of a mean, the same in every row,
+// takes no part in the rounding (a constant dloss that is no power of two would otherwise put one and the same
+// relative error into every entry -dloss of the targets, which no sum averages out).
 //
 // G lies in panels of 64 columns, [panel][token][64], so that every box of it, 64 columns x some tokens, is one
-// stretch of memory; as [token][column] a box's rows lay 2 x piece bytes apart, a
-// power of two (both gradients of 256 tokens x 131072 x 2048: 505 -> 490 us).
+// stretch of memory; as [token][column] a box's rows lay 2 x piece bytes apart, a power of two (both gradients of
+// 256 tokens x 131072 x 2048: 505 -> 490 us).
 //
 // The products are bound by the tensor cores for many tokens, under load by the power limit: the loss of 4096
 // tokens x 131072 x 2048 takes 1.67 ms one after another, 1320 TFLOP/s (the library's bf16 product that writes those
@@ -155,16 +155,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // The tensor cores' fp32 accumulator drops the bits below its last place instead of rounding them, so a long
 // sum loses up to that at each of its K / 16 steps, always toward zero.  The logits behind the loss are
-// therefore added in stretches of kVgStretch k-blocks (512 of K), each from zero, and the stretches in fp32
-// registers; the gradient's operand is rounded to bf16 and needs none of it.
-constexpr int kVgStretch = 8;
+// therefore added in stretches of VgTile::kStretch k-blocks, each from zero, and the stretches in fp32 registers;
+// the gradient's operand is rounded to bf16 and needs none of it.  Error of lse for 4096 tokens x 131072 x 2048:
+// 1.7e-6 in one stretch, 0.9e-6 in stretches of 1024 (1.67 ms both), 0.4e-6 in stretches of 512 (1.76 ms; up to 128
+// tokens, bound by HBM, it costs nothing).
 
 // Warp 0: TMA; warp 1: TMEM and, in a pair's first CTA, MMA; warps 2..9: epilogue, two per TMEM lane quarter
 // (column halves; sixteen warps on quarters, with stores of 64 instead of 128 bytes a row, made the gradients of
-// 8192 tokens 10.9 ms instead of 10.0).  Persistent: one CTA per SM, or one pair per two, walks the tiles; the accumulator is
-// buffered (two of a pair, four of a CTA), and free again
-// as soon as it is in registers.  In a pair the copies of both CTAs count on the first one's `full`, its MMAs free both
-// CTAs' stages and fill both accumulators, and both epilogues free its `tempty`.
+// 8192 tokens 10.9 ms instead of 10.0).  Persistent: one CTA per SM, or one pair per two, walks the tiles; the
+// accumulator is buffered (two of a pair, four of a CTA), and free again as soon as it is in registers.  In a pair
+// the copies of both CTAs count on the first one's `full`, its MMAs free both CTAs' stages and fill both
+// accumulators, and both epilogues free its `tempty`.
+//
 // kVgBack's tiles: dh's first, then dW's, each product with its own operands.
 struct VgMaps {
   CUtensorMap a, b, out;   // operands, and a bf16 result: boxes of 64 columns x 32 rows
