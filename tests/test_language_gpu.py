@@ -400,7 +400,7 @@ def logits_ref(h, w):
 
 
 LOSSES = [(1, 1, 64), (1, 17, 128), (7, 1000, 320), (127, 255, 64), (128, 256, 128), (129, 257, 1088), (300, 5003, 192),
-          (2, 40000, 256), (513, 999, 2048)]
+          (2, 40000, 256), (513, 999, 2048), (20, 300, 4160), (140, 300, 4160)]
 
 
 @pytest.mark.parametrize("N, V, H", LOSSES)

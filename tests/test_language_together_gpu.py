@@ -111,6 +111,28 @@ def test_a_stream_of_their_own(eng):  # noqa: F811
         assert all(torch.equal(got[k], want[k]) for k in want)
 
 
+def test_two_contexts_on_two_threads(eng):  # noqa: F811
+    """A context is not thread-safe, two contexts are independent: calls overlap on the host and on the GPU."""
+    import concurrent.futures
+    from vla_dual_expert_b200 import Engine
+    other = Engine(eng.dims, 1, 16)
+    try:
+        steps = [Step(eng, 33), Step(other, 34, B=1, T=300, V=2000, H=128)]
+        want = [s.run() for s in steps]
+        torch.cuda.synchronize()
+
+        def work(k):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got = [steps[k].run() for _ in range(10)]
+                torch.cuda.current_stream().synchronize()
+            return all(torch.equal(g[n], want[k][n]) for g in got for n in g)
+        with concurrent.futures.ThreadPoolExecutor(2) as pool:
+            assert all(pool.map(work, (0, 1)))
+        other.sync()
+    finally:
+        other.close()
+
+
 def test_launches_are_counted(eng):  # noqa: F811
     s = Step(eng, 25)
     n = eng.launch_count()

@@ -60,6 +60,7 @@ class Engine(LanguageOps):
     def __init__(self, dims, max_batch: int, max_prefix: int, time_mod: bool = False):
         """time_mod: the time-modulated action expert (DM0.5 page, section 5.2) instead of the DM0 one."""
         self.lib = load_library()
+        self._bind_language()
         self.dims = dims
         self.time_mod = bool(time_mod)
         self.cfg = make_config(dims, max_batch, max_prefix, self.time_mod)

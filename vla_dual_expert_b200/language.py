@@ -16,7 +16,10 @@ def _bind():
     global torch, _C
     if torch is None:
         import torch as t      # before the native module, which links against its libraries
-        from . import _language
+        try:
+            from . import _language
+        except ImportError as e:
+            raise ImportError(f"_language.so did not load ({e}); run `python -m vla_dual_expert_b200.build`") from e
         torch, _C = t, _language
 
 
@@ -27,8 +30,10 @@ def _handle(stream):
 class LanguageOps:
     """Mixed into Engine, whose context handle and status check it uses."""
 
+    def _bind_language(self):
+        _bind()   # before a context is made: a missing module leaves nothing behind
+
     def _open_language(self):
-        _bind()
         self.device = torch.cuda.current_device()   # the context's: the tensors of these operators live there
 
     def _done(self, r):
