@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -57,7 +58,7 @@ struct Call {
   int device;
   PyObject* given;   // the stream argument
   cudaStream_t stream;
-  bool foreign = false;   // not torch's current stream, which the allocator goes by
+  bool foreign = false;   // not torch's current stream, whose pool the allocator takes blocks from
 
   Call(PyObject* const* args, PyObject* stream_arg) : given(stream_arg) {
     ctx = static_cast<dm0_ctx*>(PyLong_AsVoidPtr(args[0]));
@@ -72,17 +73,31 @@ struct Call {
     if (PyErr_Occurred()) throw PyErr();
     foreign = stream != current;
   }
-  // a tensor of torch's allocator; on a stream that is not torch's current one it is kept until that is past it
+  // A tensor of the call's stream's own pool: the allocator hands out a block that was freed a moment ago, while
+  // kernels on the block's stream still use it, so a block of another stream's pool would be written too early.
+  Tensor take(at::IntArrayRef shape, ScalarType kind) const {
+    return at::detail::empty_cuda(shape, kind, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)),
+                                  std::nullopt);
+  }
+  // an output; the current stream is where the caller goes on, so the block is kept until that is past it too
   Tensor make(at::IntArrayRef shape, ScalarType kind) const {
-    Tensor t = at::detail::empty_cuda(shape, kind,
-                                      c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)), std::nullopt);
-    if (foreign && t.numel())
-      c10::cuda::CUDACachingAllocator::recordStream(
-          t.storage().data_ptr(),
-          c10::cuda::getStreamFromExternal(stream, static_cast<c10::DeviceIndex>(device)));
+    if (!foreign) return take(shape, kind);
+    const c10::cuda::CUDAStream here = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device));
+    const c10::cuda::CUDAStreamGuard there(target());
+    Tensor t = take(shape, kind);
+    if (t.numel()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), here);
     return t;
   }
-  Tensor scratch(size_t bytes) const { return make({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, ScalarType::Byte); }
+  // a workspace, freed when the call returns: what takes its block next follows on the same stream
+  Tensor scratch(size_t bytes) const {
+    const int64_t n = static_cast<int64_t>(bytes < 16 ? 16 : bytes);
+    if (!foreign) return take({n}, ScalarType::Byte);
+    const c10::cuda::CUDAStreamGuard there(target());
+    return take({n}, ScalarType::Byte);
+  }
+  c10::cuda::CUDAStream target() const {
+    return c10::cuda::getStreamFromExternal(stream, static_cast<c10::DeviceIndex>(device));
+  }
 
   void kind_ok(const Tensor& t, std::initializer_list<ScalarType> kinds, const char* name) const {
     if (!t.is_cuda() || t.get_device() != device || !among(t.scalar_type(), kinds))

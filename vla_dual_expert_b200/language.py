@@ -4,8 +4,10 @@ gradients (include/dm0.h has their definitions).
 Marshalling only, as the rest of the binding.  Calls on a few tokens are bound by the host, so the tensors are
 checked and the outputs and workspaces made in native code (csrc/binding.cpp, built beside libdm0.so): TypeError
 for a tensor of another type, device or layout, ValueError for another shape, Dm0Error for what the C ABI refuses.
-`stream` is a torch stream or a cudaStream_t handle; None is torch's current stream.  Tensors made by a call on
-another stream are kept by torch's allocator until that stream is past them; inputs are the caller's to keep.
+`stream` is a torch stream or a cudaStream_t handle; None is torch's current stream.  A call on another stream waits
+for nothing on the current one: its inputs, and an output that is given, have to be ready there and are the caller's
+to keep.  Its outputs and workspace come from that stream's pool; outputs are kept until both streams are past them,
+and a third stream that uses one is recorded by the caller (Tensor.record_stream), as with any tensor of torch's.
 """
 from __future__ import annotations
 
