@@ -1,0 +1,58 @@
+"""Where the vocabulary loss could lose bits: many tiles a worker, targets that the model is sure of, long sums.
+
+Tolerances count roundings in units of u = 2^-24, and are derived beside each case; the inputs are chosen so that the
+logits are exact in fp32 where the sums behind them are what is tested."""
+import math
+
+import pytest
+import torch
+
+from tests.test_language_gpu import BF, BF16, F32, U, eng, randn, rng, unwritten_memory_is_nan, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def exact_logits(N, V, H=64):
+    """hidden, weight and logits z[i][v] = c[i] x[v], x in sixteenths of 0..255, c in 64ths from 1 on: both fit bf16 and
+    one product makes each logit, so z is exact."""
+    x = torch.randint(0, 256, (V,), generator=rng(61), device="cuda") / 16
+    c = 1 + (torch.arange(N, device="cuda") % 64) / 64
+    h, w = torch.zeros(N, H, device="cuda", dtype=BF16), torch.zeros(V, H, device="cuda", dtype=BF16)
+    h[:, 0], w[:, 0] = c, x
+    assert torch.equal(h[:, 0].float(), c) and torch.equal(w[:, 0].float(), x)
+    return h, w, c[:, None].double() * x[None].double()
+
+
+@pytest.mark.parametrize("N, V", [(64, 1 << 20), (128, 500_000), (200, 1 << 20)])
+def test_statistics_keep_their_bits_over_many_tiles(eng, N, V):  # noqa: F811
+    """Up to 128 tokens a worker keeps one running (max, sum) over its tiles (2^20 entries: 56 tiles of 128 x 128 a
+    worker; 200 tokens in pairs: 56 of 256)."""
+    h, w, z = exact_logits(N, V)
+    t = torch.arange(N, device="cuda") * 977 % V
+    loss, lse = eng.vocab_loss(h, w, t)
+    ref = torch.logsumexp(z, 1)
+    # the sum: 32 additions in a chain of a tile, 2 to join the chains, 56 tiles, 3 workers a lane, 11 over the lanes and
+    # the maximum's one (104 u); an exponential and the factor of the tile (2^-22 each: 8 u); the exponents' roundings
+    # and log2 e's, u each of |z - max| log2 e, at most 20 on average over the weights, in natural units (28 u); the
+    # logarithm and the sum with the maximum (u each of at most 16 and 64: 80 u)
+    within(lse, ref, torch.full_like(ref, 220 * U), "lse")
+    picked = z.gather(1, t[:, None])[:, 0]
+    # the same with mx - z and the result rounded (u of at most 32 and 48)
+    within(loss, ref - picked, torch.full_like(ref, 220 * U), "loss")
+
+
+@pytest.mark.parametrize("N, V", [(5, 1000), (70, 40000), (200, 1000), (600, 999)])
+def test_loss_of_a_sure_token_is_not_below_zero_nor_a_unit_of_its_logit(eng, N, V):  # noqa: F811
+    """The target's logit lies 64 or more above all others: the loss is below V e^-64, whatever the logit's size."""
+    H = 64
+    h, w = torch.zeros(N, H, device="cuda", dtype=BF16), torch.zeros(V, H, device="cuda", dtype=BF16)
+    h[:, 0] = 64 + (torch.arange(N, device="cuda") % 128) / 2
+    at = V // 2 + 1
+    w[at, 0] = 1 + 1 / 128
+    t = torch.full((N,), at, device="cuda")
+    loss, lse = eng.vocab_loss(h, w, t)
+    z = h[:, 0].double() * w[at, 0].double()
+    assert (loss >= 0).all()
+    # the maximum's own term is an exponential near zero times the tile's factor near one: 2^-22 each, their rounding
+    within(loss, torch.zeros_like(z), torch.full_like(z, 2 ** -21 + 4 * U), "loss")
+    within(lse, z, 2 ** -21 + U * (z + 4), "lse")
