@@ -56,3 +56,45 @@ def test_loss_of_a_sure_token_is_not_below_zero_nor_a_unit_of_its_logit(eng, N, 
     # the maximum's own term is an exponential near zero times the tile's factor near one: 2^-22 each, their rounding
     within(loss, torch.zeros_like(z), torch.full_like(z, 2 ** -21 + 4 * U), "loss")
     within(lse, z, 2 ** -21 + U * (z + 4), "lse")
+
+
+@pytest.mark.parametrize("N, V, H", [(40, 2000, 2048), (300, 2000, 2048), (300, 1999, 1088), (24, 700, 4160)])
+def test_gradient_of_sure_tokens(eng, N, V, H):  # noqa: F811
+    """Tokens whose target has all but 1e-2 to 1e-5 of the probability: each one's row of dhidden against its own size.
+    The reference is the definition in 64 bits; the kernels' lse takes the place of its own."""
+    g = rng(62)
+    w = randn(g, V, H, dtype=BF16, std=0.9 * H ** -0.5)
+    t = torch.arange(N, device="cuda") * 31 % V
+    wt = w[t].float()
+    size = torch.linspace(13.5, 22, N, device="cuda")[:, None]
+    h = (randn(g, N, H) + size * wt / wt.norm(dim=1, keepdim=True)).to(BF16)
+    loss, lse = eng.vocab_loss(h, w, t)
+    dh, _ = eng.vocab_loss_grad(h, w, t, lse, torch.ones(N, device="cuda"), dhidden=torch.empty(N, H, device="cuda"),
+                                dweight=False)
+    hd, wd = h.double(), w.double()
+    z = hd @ wd.T
+    p = torch.softmax(z, 1)
+    rest = p.scatter(1, t[:, None], 0.0)          # the others' probabilities
+    q = rest.sum(1, keepdim=True)                 # 1 - p of the target
+    assert q.max() > 3e-3 and q.min() < 3e-5
+    G = rest.scatter(1, t[:, None], -q)
+    # a logit: products exact, 1024 / 16 additions of up to 2 u in a stretch (and 16 to spare), then the stretches in fp32
+    ez = (2 * U * (64 + 16) + U * H / 512) * (hd.abs() @ wd.abs().T)
+    # another entry: its logit's and the target's error against it, exp's 2^-22 and four roundings of exponents below 64
+    eo = rest * (ez + ez.gather(1, t[:, None]) + 2 ** -21 + 4 * U * (z.abs() + lse.double().abs()[:, None]))
+    # the target: 1 - p = 1 - exp(z - lse) takes the same relative errors, as lse is that of the same logits, and what
+    # the sum that holds a term of one may lose (32 additions of a chain, 2 and 1 to join, 12 over tiles and lanes, the
+    # term itself 2^-21: 55 u) and lse's rounding (u of at most 32)
+    et = q * (2 * ez.amax(1, keepdim=True) + 2 ** -20) + (55 + 32) * U
+    eG = eo.scatter(1, t[:, None], et)
+    eG = eG + BF * (G.abs() + eG) + 2.0 ** -126
+    ref = G @ wd
+    bound = eG @ wd.abs() + 2 * U * (V / 16 + 64) * (G.abs() @ wd.abs())
+    within(dh, ref, bound + U * (ref.abs() + bound), "dhidden")
+    rel = (dh.double() - ref).norm(dim=1) / ref.norm(dim=1)
+    for lo, hi in ((3e-3, 1), (1e-3, 3e-3), (1e-4, 1e-3), (1e-5, 1e-4)):
+        rows = ((q >= lo) & (q < hi))[:, 0]
+        print(f"  1 - p from {lo:.0e}: rows off by up to", f"{rel[rows].max().item():.1e}" if rows.any() else "-")
+    # in the whole row the others' errors go in all directions: a row is off by little more than its target's entry
+    lim = et[:, 0] / q[:, 0] + 2 * BF
+    assert (rel <= lim).all()

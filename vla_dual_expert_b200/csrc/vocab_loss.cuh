@@ -106,17 +106,18 @@ __device__ __forceinline__ void vg_scratch_free() {
 // scheduler, so its instructions count: addresses by one exclusive or, paired multiplications, one accumulator load
 // per chunk, and no loads and stores of the rows by the warp.
 template <bool PANEL>
-__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&v)[64], const CUtensorMap* map, int x, int y,
-                                              int rows) {
+__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float* lo, const float* hi, const CUtensorMap* map,
+                                              int x, int y, int rows) {
   const int lane = threadIdx.x & 31;
   vg_scratch_free();
   const uint32_t w = smem_u32(scr) + lane * 128 + ((lane & 7) << 4);   // scr is 1024-byte aligned
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(w ^ (j << 4)), "r"(bf2(v[8 * j], v[8 * j + 1])),
-                 "r"(bf2(v[8 * j + 2], v[8 * j + 3])), "r"(bf2(v[8 * j + 4], v[8 * j + 5])),
-                 "r"(bf2(v[8 * j + 6], v[8 * j + 7]))
+  for (int j = 0; j < 8; ++j) {
+    const float* v = (j < 4 ? lo : hi) + 8 * (j & 3);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(w ^ (j << 4)), "r"(bf2(v[0], v[1])),
+                 "r"(bf2(v[2], v[3])), "r"(bf2(v[4], v[5])), "r"(bf2(v[6], v[7]))
                  : "memory");
+  }
   fence_async_smem();
   __syncwarp();
   if (lane == 0 && rows > 0) {
@@ -154,11 +155,14 @@ __device__ __forceinline__ void vg_store_f32(uint8_t* scr, const float* v, float
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The tensor cores' fp32 accumulator drops the bits below its last place instead of rounding them, so a long
-// sum loses up to that at each of its K / 16 steps, always toward zero.  The logits behind the loss are
-// therefore added in stretches of VgTile::kStretch k-blocks, each from zero, and the stretches in fp32 registers;
-// the gradient's operand is rounded to bf16 and needs none of it.  Error of lse for 4096 tokens x 131072 x 2048:
-// 1.7e-6 in one stretch, 0.9e-6 in stretches of 1024 (1.67 ms both), 0.4e-6 in stretches of 512 (1.76 ms; up to 128
-// tokens, bound by HBM, it costs nothing).
+// sum loses up to that at each of its K / 16 steps, always toward zero.  The logits are therefore added in
+// stretches of VgTile::kStretch k-blocks, each from zero, and the stretches in fp32 registers.  Error of lse for 4096
+// tokens x 131072 x 2048: 1.7e-6 in one stretch, 0.9e-6 in stretches of 1024 (1.67 ms both), 0.4e-6 in stretches of
+// 512 (1.76 ms; up to 128 tokens, bound by HBM, it costs nothing).
+// The gradient builds the same logits bit for bit.  Of a target that the model is sure of, exp(z - lse) - 1 is all
+// cancellation: there the logit's error has to be the one that lse has, and the difference one function, expm1 (in one
+// stretch and as a difference such rows of dhidden came out up to several times too large at 1 - p = 1e-5; it costs the
+// gradients of 8192 tokens 1%, of 700 tokens x 11000 x 512, mostly epilogue, 5%: 41.2 -> 43.5 us).
 
 // Warp 0: TMA; warp 1: TMEM and, in a pair's first CTA, MMA; warps 2..9: epilogue, two per TMEM lane quarter
 // (column halves; sixteen warps on quarters, with stores of 64 instead of 128 bytes a row, made the gradients of
@@ -239,7 +243,7 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
     w.kb1 = min((a.K + 63) >> 6, w.kb0 + a.kb_per_split);
     return w;
   };
-  auto stretch_end = [&](int kb, int kb1) { return MODE == kVgStats ? min(kb1, kb + kStretch) : kb1; };
+  auto stretch_end = [&](int kb, int kb1) { return MODE != kVgBack ? min(kb1, kb + kStretch) : kb1; };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -430,8 +434,8 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
         if (tgt >= a.vocab) tgt = -1;
         if (MODE == kVgGrad) row_lse = a.lse[row], row_dloss = a.dloss[row];
       }
-      if constexpr (MODE == kVgStats) {
-        float v[kCols / 32][32];
+      float v[MODE != kVgBack ? kCols / 32 : 1][32];   // logits of this row
+      if constexpr (MODE != kVgBack) {
         for (int ks = w.kb0; ks < w.kb1; ks = stretch_end(ks, w.kb1)) {
           if (!ready()) {
             go = false;
@@ -453,6 +457,8 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           release();
         }
         if (!go) break;
+      }
+      if constexpr (MODE == kVgStats) {
         if (col0 + kCols > a.valid_n) {
 #pragma unroll
           for (int c = 0; c < kCols / 32; ++c)
@@ -497,37 +503,40 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           run_mx = now.x, run_sum = now.y;
           if (q + 1 == mine && row < a.M) a.part[static_cast<int64_t>(2 * worker + half) * a.part_ld + row] = now;
         }
+      } else if constexpr (MODE == kVgGrad) {
+        const float l2 = row_lse * kLog2e, gi = row_dloss / s;
+        const int rel = tgt - a.v0 - col0;   // place of the target among v (maybe outside)
+        const int last = tgt < 0 ? 0 : a.valid_n - col0;   // places from here on are zero
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          float at = 0.f;   // the target's value
+          const bool here = static_cast<unsigned>(rel - 32 * c) < 32u;
+          if (here) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) at = rel == 32 * c + j ? v[c][j] : at;
+            at = expm1f(at - row_lse) * gi;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float2 x = ffma2(make_float2(v[c][j], v[c][j + 1]), make_float2(kLog2e, kLog2e), make_float2(-l2, -l2));
+            const float2 p = fmul2(make_float2(ex2_fast(x.x), ex2_fast(x.y)), make_float2(gi, gi));
+            v[c][j] = p.x, v[c][j + 1] = p.y;
+          }
+          if (here) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (rel == 32 * c + j) v[c][j] = at;
+          }
+          if (32 * c + 32 > last) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[c][j] = 32 * c + j >= last ? 0.f : v[c][j];
+          }
+          if (c & 1) vg_store_bf16<true>(scr, v[c - 1], v[c], &m0.out, col0 + 32 * (c - 1), row0, rows);
+        }
       } else {
         if (!ready()) break;
         const uint32_t tm = tm0 + (local % kBufs) * kN;
-        if constexpr (MODE == kVgGrad) {
-          const float l2 = row_lse * kLog2e, gi = row_dloss / s;
-          const int rel = tgt - a.v0;   // column of the target in this piece (maybe outside)
-#pragma unroll 1
-          for (int c = 0; c < kCols / 64; ++c) {
-            float v[64];
-            tmem_ld64(tm + 64 * c, v);
-            if (c + 1 == kCols / 64) release();
-            const int cc = col0 + 64 * c;
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-              const float2 x = ffma2(make_float2(v[j], v[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-l2, -l2));
-              const float2 p = fmul2(make_float2(ex2_fast(x.x), ex2_fast(x.y)), make_float2(gi, gi));
-              v[j] = p.x, v[j + 1] = p.y;
-            }
-            if (static_cast<unsigned>(rel - cc) < 64u) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j)
-                if (rel - cc == j) v[j] -= gi;
-            }
-            if (tgt < 0 || cc + 64 > a.valid_n) {
-#pragma unroll
-              for (int j = 0; j < 64; ++j)
-                if (tgt < 0 || cc + j >= a.valid_n) v[j] = 0.f;
-            }
-            vg_store_bf16<true>(scr, v, &m0.out, cc, row0, rows);
-          }
-        } else if (!w.second) {
+        if (!w.second) {
           vg_scratch_free();
           float* dst = a.dh + (static_cast<int64_t>(w.split) * a.M + row0) * a.N + col0;
 #pragma unroll 1
@@ -555,7 +564,7 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
               vg_store_f32(scr, v, dst, a.N, rows, a.add != 0);
               vg_store_f32(scr, v + 32, dst + 32, a.N, rows, a.add != 0);
             } else {
-              vg_store_bf16<false>(scr, v, &m1.out, col0 + 64 * c, a.v0 + row0, rows);
+              vg_store_bf16<false>(scr, v, v + 32, &m1.out, col0 + 64 * c, a.v0 + row0, rows);
             }
           }
         }
