@@ -98,3 +98,46 @@ def test_gradient_of_sure_tokens(eng, N, V, H):  # noqa: F811
     # in the whole row the others' errors go in all directions: a row is off by little more than its target's entry
     lim = et[:, 0] / q[:, 0] + 2 * BF
     assert (rel <= lim).all()
+
+
+@pytest.mark.parametrize("N, dt", [(1 << 17, F32), (1 << 17, BF16), (40000, F32)])
+def test_weight_gradient_of_many_tokens(eng, N, dt):  # noqa: F811
+    """Sums of one sign over all tokens: G is 2^-8, and 2^-8 - 1 at the target, both exact in bf16, so only the sums round."""
+    V, H = 256, 64
+    h = (1 + torch.rand(N, H, generator=rng(63), device="cuda")).to(BF16)
+    w = torch.zeros(V, H, device="cuda", dtype=BF16)
+    t = torch.zeros(N, dtype=torch.int64, device="cuda")
+    lse = torch.full((N,), math.log(V), device="cuda")
+    _, dw = eng.vocab_loss_grad(h, w, t, lse, torch.ones(N, device="cuda"), dhidden=False,
+                                dweight=torch.empty(V, H, device="cuda", dtype=dt))
+    total = h.double().sum(0)
+    ref = (total / V).expand(V, H).clone()
+    ref[0] -= total
+    # 16384 / 16 additions of up to 2 u in a stretch (and 16 to spare), then the stretches in fp32, and the factor of one
+    k = 2 * (1024 + 16) + math.ceil(N / 16384) + 1
+    within(dw, ref, ref.abs() * (k * U + (BF if dt == BF16 else U) * (1 + k * U)), "dweight")
+    old = torch.full((V, H), 3.0, device="cuda")
+    if dt == F32:
+        _, acc = eng.vocab_loss_grad(h, w, t, lse, torch.ones(N, device="cuda"), dhidden=False, dweight=old.clone(),
+                                     accumulate=True)
+        within(acc, ref + 3, ref.abs() * k * U + (ref + 3).abs() * 2 * U, "accumulated")
+
+
+@pytest.mark.parametrize("N, V", [(1, 1 << 22), (300, 400_000)])
+def test_hidden_gradient_over_a_long_vocabulary(eng, N, V):  # noqa: F811
+    """Equal logits: G is 1 / V but at the target, and weights of one sign add up over the whole vocabulary."""
+    H = 64
+    w = (1 + torch.rand(V, H, generator=rng(64), device="cuda")).to(BF16)
+    h = torch.zeros(N, H, device="cuda", dtype=BF16)
+    t = torch.arange(N, device="cuda") * 7919 % V
+    loss, lse = eng.vocab_loss(h, w, t)
+    dh, _ = eng.vocab_loss_grad(h, w, t, lse, torch.ones(N, device="cuda"), dhidden=torch.empty(N, H, device="cuda"),
+                                dweight=False)
+    g = torch.tensor(1 / V).to(BF16).double().item()   # every entry's rounding to bf16 is the same; the target's is 1 - 1 / V
+    others = g * (w.double().sum(0) - w[t].double())
+    one = torch.tensor(1 - 1 / V).to(BF16).double().item()
+    ref, mag = others - one * w[t].double(), others.abs() + one * w[t].double()
+    # a stretch as above, and the splits (at most 256) and pieces (at most 2) in fp32; an exponential that is 2^-21 off
+    # falls to another bf16 only where 1 / V lies that near to a border
+    assert abs(abs((1 / V) / g - 1) - BF / 2) > 2 ** -19 or g * V == 1
+    within(dh, ref, mag * (2 * (1024 + 16) + 256 + 2 + 4) * U, "dhidden")

@@ -252,8 +252,10 @@ VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
   const int cols = std::min(p.piece, vocab);
   const int64_t ht = (H + tile - 1) / tile, th = (tokens + tile - 1) / tile * ht, tw = (cols + tile - 1) / tile * ht;
   const int KB = (cols + 63) / 64, KW = (tokens + 63) / 64;   // of the first piece, whose splits all write
+  // (a split is one stretch of the accumulator: at most kVgBackStretch k-blocks)
   double best = 0;
-  for (int S = 1; S <= std::min(KB, 64); ++S) {
+  const int least = (KB + dm0::kVgBackStretch - 1) / dm0::kVgBackStretch;
+  for (int S = least; S <= std::max(least, std::min(KB, 64)); ++S) {
     const int per = (KB + S - 1) / S, used = (KB + per - 1) / per;
     if (used != S) continue;
     double busiest = 0;
@@ -264,7 +266,7 @@ VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
       busiest = std::max(busiest, mine * (per * 0.28 + 1.0) + (all - mine) * (KW * 0.28 + 1.0));
     }
     const double t = busiest + S * 8.0 * tokens * H / 6.0e6;
-    if (S == 1 || t < best) best = t, p.splits = S, p.kb_per_split = per;
+    if (!p.splits || t < best) best = t, p.splits = S, p.kb_per_split = per;
   }
   p.scale = 0;
   p.g = 256;
@@ -289,14 +291,18 @@ dm0_status vocab_grid(dm0_ctx* c, bool pairs, int64_t tiles, dim3* grid) {
                 : dim3(static_cast<unsigned>(std::min<int64_t>(tiles, c->num_sms)));
   return DM0_OK;
 }
+bool vocab_long(bool pairs, int H) {
+  return H > 64 * (pairs ? dm0::VgTile<true>::kStretch : dm0::VgTile<false>::kStretch);
+}
 int64_t vocab_tiles(const dm0::VgArgs& a) { return static_cast<int64_t>(a.mt) * a.nt * a.splits; }
 
-template <int MODE>
+// LONG: the contraction takes more than one stretch of the accumulator
+template <int MODE, bool LONG>
 dm0_status vocab_gemm(dm0_ctx* c, cudaStream_t s, bool pairs, const dm0::VgMaps& m, const dm0::VgArgs& a) {
   dim3 grid;
   TRY(vocab_grid(c, pairs, vocab_tiles(a), &grid));
-  if (pairs) return launch(c, s, dm0::vocab_gemm_pair_kernel<MODE>, grid, dim3(320), dm0::VgTile<true>::kBytes, m, a);
-  return launch(c, s, dm0::vocab_gemm_kernel<MODE>, grid, dim3(320), dm0::VgTile<false>::kBytes, m, a);
+  if (pairs) return launch(c, s, dm0::vocab_gemm_pair_kernel<MODE, LONG>, grid, dim3(320), dm0::VgTile<true>::kBytes, m, a);
+  return launch(c, s, dm0::vocab_gemm_kernel<MODE, LONG>, grid, dim3(320), dm0::VgTile<false>::kBytes, m, a);
 }
 
 dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16* w, dm0::Ids tgt, int tokens, int vocab,
@@ -324,7 +330,7 @@ dm0_status vocab_loss_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.part_ld = p.part_ld;
   a.zt = reinterpret_cast<float*>(ws + p.zt);
-  TRY(vocab_gemm<dm0::kVgStats>(c, s, pairs, m, a));
+  TRY((vocab_gemm<dm0::kVgStats, true>(c, s, pairs, m, a)));
   const int parts = 2 * (p.mt > 1 ? p.nt : std::min(p.nt, pairs ? c->num_sms / 2 : c->num_sms));
   return launch(c, s, dm0::vocab_loss_kernel, dim3((tokens + 3) / 4), dim3(512), 0,
                 static_cast<const float2*>(a.part), parts, p.part_ld, static_cast<const float*>(a.zt), tgt, tokens,
@@ -373,7 +379,8 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
     a.valid_n = cols;
     a.lse = lse;
     a.dloss = dloss;
-    TRY(vocab_gemm<dm0::kVgGrad>(c, s, pairs, mg, a));
+    TRY((vocab_long(pairs, H) ? vocab_gemm<dm0::kVgGrad, true>(c, s, pairs, mg, a)
+                              : vocab_gemm<dm0::kVgGrad, false>(c, s, pairs, mg, a)));
     dm0::VgArgs ah = a, aw = a;
     ah.N = H;
     ah.K = cols;
@@ -397,8 +404,10 @@ dm0_status vocab_grad_run(dm0_ctx* c, cudaStream_t s, const bf16* h, const bf16*
     aw.dw = dw_f32 ? static_cast<float*>(dw) : nullptr;
     dim3 grid;
     TRY(vocab_grid(c, pairs, vocab_tiles(ah) + vocab_tiles(aw), &grid));
+    const bool many = tokens > 64 * dm0::kVgBackStretch;   // so dW takes several stretches
     if (pairs)
-      TRY(launch(c, s, dm0::vocab_back_pair_kernel, grid, dim3(320), dm0::VgTile<true>::kBytes, mh, ah, mw, aw));
+      TRY(launch(c, s, many ? dm0::vocab_back_pair_kernel<true> : dm0::vocab_back_pair_kernel<false>, grid, dim3(320),
+                 dm0::VgTile<true>::kBytes, mh, ah, mw, aw));
     else
       TRY(launch(c, s, dm0::vocab_back_kernel, grid, dim3(320), dm0::VgTile<false>::kBytes, mh, ah, mw, aw));
   }
@@ -425,12 +434,15 @@ bool lang_setup() {
          norm_grad_setup<bf16, bf16, f>() && norm_grad_setup<bf16, bf16, bf16>() &&
          attr(dm0::embed_sort_kernel<int>, 4 * dm0::kSortWarps * (dm0::kSortMaxRows + dm0::kSortList)) &&
          attr(dm0::embed_sort_kernel<long long>, 4 * dm0::kSortWarps * (dm0::kSortMaxRows + dm0::kSortList)) &&
-         attr(dm0::vocab_gemm_kernel<dm0::kVgStats>, dm0::VgTile<false>::kBytes) &&
-         attr(dm0::vocab_gemm_kernel<dm0::kVgGrad>, dm0::VgTile<false>::kBytes) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgStats, true>, dm0::VgTile<false>::kBytes) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgGrad, false>, dm0::VgTile<false>::kBytes) &&
+         attr(dm0::vocab_gemm_kernel<dm0::kVgGrad, true>, dm0::VgTile<false>::kBytes) &&
          attr(dm0::vocab_back_kernel, dm0::VgTile<false>::kBytes) &&
-         attr(dm0::vocab_gemm_pair_kernel<dm0::kVgStats>, dm0::VgTile<true>::kBytes) &&
-         attr(dm0::vocab_gemm_pair_kernel<dm0::kVgGrad>, dm0::VgTile<true>::kBytes) &&
-         attr(dm0::vocab_back_pair_kernel, dm0::VgTile<true>::kBytes);
+         attr(dm0::vocab_gemm_pair_kernel<dm0::kVgStats, true>, dm0::VgTile<true>::kBytes) &&
+         attr(dm0::vocab_gemm_pair_kernel<dm0::kVgGrad, false>, dm0::VgTile<true>::kBytes) &&
+         attr(dm0::vocab_gemm_pair_kernel<dm0::kVgGrad, true>, dm0::VgTile<true>::kBytes) &&
+         attr(dm0::vocab_back_pair_kernel<false>, dm0::VgTile<true>::kBytes) &&
+         attr(dm0::vocab_back_pair_kernel<true>, dm0::VgTile<true>::kBytes);
 }
 }  // namespace
 

@@ -27,7 +27,7 @@
 // weights, 82 at the rate of a copy); the gradient twice, as its second product needs G's whole rows, and dW is
 // written (316 us, 245 at that rate).
 #pragma once
-#include "attention_tc.cuh"   // sw128_mnmajor_desc
+#include "attention_tc.cuh"   // sw128_mnmajor_desc, tmem_st32
 #include "embedding.cuh"
 #include "gemm.cuh"           // band_tile, resid_swz, bf2
 #include "residual_norm.cuh"  // store4
@@ -64,6 +64,8 @@ struct VgArgs {
   float* dw;            // [vocab][H] in fp32; null: bf16 through the map
 };
 
+constexpr int kVgBackStretch = 256;   // k-blocks of the gradients' products added in the accumulator
+
 // Tile of a CTA pair (cta_group::2): 256 rows of A times 256 rows of B, of which each CTA stages half.  Tile of
 // one CTA, for up to 128 tokens, where a product is one read of W: 128 x 128, narrow so that the tiles of a
 // vocabulary spread evenly (131072 columns, 148 SMs: 7 rounds of 128, 99% busy, against 4 of 256, 86%).
@@ -73,7 +75,7 @@ struct VgTile {
   static constexpr int kBRows = 128;   // of B, per CTA
   static constexpr int kStages = 6;
   static constexpr int kBufs = 512 / kN;   // accumulators in TMEM
-  static constexpr int kStretch = PAIR ? 16 : 8;   // k-blocks of the loss's logits added in the accumulator
+  static constexpr int kStretch = PAIR ? 16 : 8;   // k-blocks of logits added in the accumulator
   static constexpr uint32_t kA = 128 * 128, kB = kBRows * 128, kStage = kA + kB, kPipe = kStages * kStage;
   static constexpr uint32_t kScr = kPipe;                 // 8 x 4 KB
   static constexpr uint32_t kBar = kScr + 8 * 4096;
@@ -106,18 +108,21 @@ __device__ __forceinline__ void vg_scratch_free() {
 // scheduler, so its instructions count: addresses by one exclusive or, paired multiplications, one accumulator load
 // per chunk, and no loads and stores of the rows by the warp.
 template <bool PANEL>
-__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float* lo, const float* hi, const CUtensorMap* map,
-                                              int x, int y, int rows) {
+__device__ __forceinline__ void vg_store_bf16(uint8_t* scr, const float (&v)[64], const CUtensorMap* map, int x, int y,
+                                              int rows, int place = -1, float at = 0.f) {
   const int lane = threadIdx.x & 31;
   vg_scratch_free();
   const uint32_t w = smem_u32(scr) + lane * 128 + ((lane & 7) << 4);   // scr is 1024-byte aligned
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float* v = (j < 4 ? lo : hi) + 8 * (j & 3);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(w ^ (j << 4)), "r"(bf2(v[0], v[1])),
-                 "r"(bf2(v[2], v[3])), "r"(bf2(v[4], v[5])), "r"(bf2(v[6], v[7]))
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(w ^ (j << 4)), "r"(bf2(v[8 * j], v[8 * j + 1])),
+                 "r"(bf2(v[8 * j + 2], v[8 * j + 3])), "r"(bf2(v[8 * j + 4], v[8 * j + 5])),
+                 "r"(bf2(v[8 * j + 6], v[8 * j + 7]))
                  : "memory");
-  }
+  if (place >= 0)   // this row's value there is another
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"((w ^ ((place >> 3) << 4)) + 2 * (place & 7)),
+                 "h"(static_cast<uint16_t>(bf2(at, 0.f)))
+                 : "memory");
   fence_async_smem();
   __syncwarp();
   if (lane == 0 && rows > 0) {
@@ -161,8 +166,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 512 (1.76 ms; up to 128 tokens, bound by HBM, it costs nothing).
 // The gradient builds the same logits bit for bit.  Of a target that the model is sure of, exp(z - lse) - 1 is all
 // cancellation: there the logit's error has to be the one that lse has, and the difference one function, expm1 (in one
-// stretch and as a difference such rows of dhidden came out up to several times too large at 1 - p = 1e-5; it costs the
-// gradients of 8192 tokens 1%, of 700 tokens x 11000 x 512, mostly epilogue, 5%: 41.2 -> 43.5 us).
+// stretch and as a difference, rows of dhidden were off by up to 23% at 1 - p from 1e-4 to 1e-3, and by three times
+// themselves below).
+// The gradients' products take stretches of kVgBackStretch k-blocks: a split of dh is at most one, dW of more than
+// 16384 tokens several (LONG; 2^17 tokens of one sign in one stretch: 8e-4 off).
 
 // Warp 0: TMA; warp 1: TMEM and, in a pair's first CTA, MMA; warps 2..9: epilogue, two per TMEM lane quarter
 // (column halves; sixteen warps on quarters, with stores of 64 instead of 128 bytes a row, made the gradients of
@@ -175,10 +182,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct VgMaps {
   CUtensorMap a, b, out;   // operands, and a bf16 result: boxes of 64 columns x 32 rows
 };
-template <int MODE, bool PAIR>
+template <int MODE, bool PAIR, bool LONG>
 __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, const VgMaps& m1, const VgArgs& a1) {
   using L = VgTile<PAIR>;
-  constexpr int kStages = L::kStages, kN = L::kN, kBufs = L::kBufs, kStretch = L::kStretch;
+  constexpr int kStages = L::kStages, kN = L::kN, kBufs = L::kBufs;
+  constexpr int kStretch = MODE == kVgBack ? kVgBackStretch : L::kStretch;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -243,7 +251,7 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
     w.kb1 = min((a.K + 63) >> 6, w.kb0 + a.kb_per_split);
     return w;
   };
-  auto stretch_end = [&](int kb, int kb1) { return MODE != kVgBack ? min(kb1, kb + kStretch) : kb1; };
+  auto stretch_end = [&](int kb, int kb1) { return LONG ? min(kb1, kb + kStretch) : kb1; };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -418,6 +426,34 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
       ++local;
     };
     const uint32_t tm0 = tmem + (static_cast<uint32_t>(lane_base) << 16) + half * kCols;
+    // The next accumulator holds the tile's whole sum: those of more stretches are added in registers, and go back to the
+    // last one's place, from where all tiles are read alike, a few columns at a time.
+    auto whole = [&](const Tile& w) {
+      if (!ready()) return false;
+      if (!LONG || w.kb1 - w.kb0 <= kStretch) return true;
+      float v[kCols / 32][32];
+#pragma unroll
+      for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tm0 + (local % kBufs) * kN + 32 * c, v[c]);
+      release();
+      for (int ks = stretch_end(w.kb0, w.kb1);; ks = stretch_end(ks, w.kb1)) {
+        if (!ready()) return false;
+        const bool last = ks + kStretch >= w.kb1;
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          const uint32_t at = tm0 + (local % kBufs) * kN + 32 * c;
+          float x[32];
+          tmem_ld32(at, x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[c][j] += x[j];
+          if (last) tmem_st32(at, v[c]);
+        }
+        if (last) {
+          tmem_wait_st();
+          return true;
+        }
+        release();
+      }
+    };
     bool go = true;
     float run_mx = -INFINITY, run_sum = 0.f;   // of kVgStats with one m-tile
     for (int q = 0; go && q < mine; ++q) {
@@ -434,8 +470,8 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
         if (tgt >= a.vocab) tgt = -1;
         if (MODE == kVgGrad) row_lse = a.lse[row], row_dloss = a.dloss[row];
       }
-      float v[MODE != kVgBack ? kCols / 32 : 1][32];   // logits of this row
-      if constexpr (MODE != kVgBack) {
+      if constexpr (MODE == kVgStats) {
+        float v[kCols / 32][32];
         for (int ks = w.kb0; ks < w.kb1; ks = stretch_end(ks, w.kb1)) {
           if (!ready()) {
             go = false;
@@ -457,8 +493,6 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           release();
         }
         if (!go) break;
-      }
-      if constexpr (MODE == kVgStats) {
         if (col0 + kCols > a.valid_n) {
 #pragma unroll
           for (int c = 0; c < kCols / 32; ++c)
@@ -503,40 +537,39 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
           run_mx = now.x, run_sum = now.y;
           if (q + 1 == mine && row < a.M) a.part[static_cast<int64_t>(2 * worker + half) * a.part_ld + row] = now;
         }
-      } else if constexpr (MODE == kVgGrad) {
-        const float l2 = row_lse * kLog2e, gi = row_dloss / s;
-        const int rel = tgt - a.v0 - col0;   // place of the target among v (maybe outside)
-        const int last = tgt < 0 ? 0 : a.valid_n - col0;   // places from here on are zero
-#pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-          float at = 0.f;   // the target's value
-          const bool here = static_cast<unsigned>(rel - 32 * c) < 32u;
-          if (here) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) at = rel == 32 * c + j ? v[c][j] : at;
-            at = expm1f(at - row_lse) * gi;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 x = ffma2(make_float2(v[c][j], v[c][j + 1]), make_float2(kLog2e, kLog2e), make_float2(-l2, -l2));
-            const float2 p = fmul2(make_float2(ex2_fast(x.x), ex2_fast(x.y)), make_float2(gi, gi));
-            v[c][j] = p.x, v[c][j + 1] = p.y;
-          }
-          if (here) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (rel == 32 * c + j) v[c][j] = at;
-          }
-          if (32 * c + 32 > last) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[c][j] = 32 * c + j >= last ? 0.f : v[c][j];
-          }
-          if (c & 1) vg_store_bf16<true>(scr, v[c - 1], v[c], &m0.out, col0 + 32 * (c - 1), row0, rows);
-        }
       } else {
-        if (!ready()) break;
+        if (!whole(w)) break;
         const uint32_t tm = tm0 + (local % kBufs) * kN;
-        if (!w.second) {
+        if constexpr (MODE == kVgGrad) {
+          const float l2 = row_lse * kLog2e, gi = row_dloss / s;
+          const int rel = tgt - a.v0;   // column of the target in this piece (maybe outside)
+#pragma unroll 1
+          for (int c = 0; c < kCols / 64; ++c) {
+            float v[64];
+            tmem_ld64(tm + 64 * c, v);
+            if (c + 1 == kCols / 64) release();
+            const int cc = col0 + 64 * c;
+            const bool here = static_cast<unsigned>(rel - cc) < 64u;
+            float at = 0.f;   // the target's value
+            if (here) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) at = rel - cc == j ? v[j] : at;
+              at = expm1f(at - row_lse) * gi;
+            }
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+              const float2 x = ffma2(make_float2(v[j], v[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-l2, -l2));
+              const float2 p = fmul2(make_float2(ex2_fast(x.x), ex2_fast(x.y)), make_float2(gi, gi));
+              v[j] = p.x, v[j + 1] = p.y;
+            }
+            if (tgt < 0 || cc + 64 > a.valid_n) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (tgt < 0 || cc + j >= a.valid_n) v[j] = 0.f;
+            }
+            vg_store_bf16<true>(scr, v, &m0.out, cc, row0, rows, here ? rel - cc : -1, at);
+          }
+        } else if (!w.second) {
           vg_scratch_free();
           float* dst = a.dh + (static_cast<int64_t>(w.split) * a.M + row0) * a.N + col0;
 #pragma unroll 1
@@ -564,7 +597,7 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
               vg_store_f32(scr, v, dst, a.N, rows, a.add != 0);
               vg_store_f32(scr, v + 32, dst + 32, a.N, rows, a.add != 0);
             } else {
-              vg_store_bf16<false>(scr, v, v + 32, &m1.out, col0 + 64 * c, a.v0 + row0, rows);
+              vg_store_bf16<false>(scr, v, &m1.out, col0 + 64 * c, a.v0 + row0, rows);
             }
           }
         }
@@ -584,25 +617,26 @@ __device__ __forceinline__ void vocab_gemm(const VgMaps& m0, const VgArgs& a0, c
   }
 }
 
-template <int MODE>
+template <int MODE, bool LONG>
 __global__ void __launch_bounds__(320, 1)
     vocab_gemm_kernel(const __grid_constant__ VgMaps m, const __grid_constant__ VgArgs a) {
-  vocab_gemm<MODE, false>(m, a, m, a);
+  vocab_gemm<MODE, false, LONG>(m, a, m, a);
 }
-template <int MODE>
+template <int MODE, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
     vocab_gemm_pair_kernel(const __grid_constant__ VgMaps m, const __grid_constant__ VgArgs a) {
-  vocab_gemm<MODE, true>(m, a, m, a);
+  vocab_gemm<MODE, true, LONG>(m, a, m, a);
 }
 __global__ void __launch_bounds__(320, 1)
     vocab_back_kernel(const __grid_constant__ VgMaps mh, const __grid_constant__ VgArgs ah,
                       const __grid_constant__ VgMaps mw, const __grid_constant__ VgArgs aw) {
-  vocab_gemm<kVgBack, false>(mh, ah, mw, aw);
+  vocab_gemm<kVgBack, false, false>(mh, ah, mw, aw);
 }
+template <bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
     vocab_back_pair_kernel(const __grid_constant__ VgMaps mh, const __grid_constant__ VgArgs ah,
                            const __grid_constant__ VgMaps mw, const __grid_constant__ VgArgs aw) {
-  vocab_gemm<kVgBack, true>(mh, ah, mw, aw);
+  vocab_gemm<kVgBack, true, LONG>(mh, ah, mw, aw);
 }
 
 // The tiles' (max, sum) joined: a block has 4 tokens (one 32-byte sector of `part` a tile) x 128 lanes of tiles,
