@@ -550,6 +550,9 @@ dm0_status dm0_clear_error(dm0_ctx* ctx);
 /* Human-readable description of the last failure on `ctx` (never NULL). */
 const char* dm0_last_error(const dm0_ctx* ctx);
 
+/* CUDA device that was current at dm0_create (-1 without a context). */
+int dm0_device(const dm0_ctx* ctx);
+
 /* Free everything the context owns.  NULL is ignored. */
 void dm0_destroy(dm0_ctx* ctx);
 

@@ -60,7 +60,6 @@ class Engine(LanguageOps):
     def __init__(self, dims, max_batch: int, max_prefix: int, time_mod: bool = False):
         """time_mod: the time-modulated action expert (DM0.5 page, section 5.2) instead of the DM0 one."""
         self.lib = load_library()
-        self._bind_language()
         self.dims = dims
         self.time_mod = bool(time_mod)
         self.cfg = make_config(dims, max_batch, max_prefix, self.time_mod)
@@ -69,7 +68,7 @@ class Engine(LanguageOps):
         if st != 0 or not h.value:
             raise Dm0Error(st, "dm0_create failed (configuration or device allocation)")
         self.h = h
-        self._open_language()
+        self.device = self.lib.dm0_device(h)   # the tensors of the language operators live there
 
     # ------------------------------------------------------------------ helpers
     def _chk(self, st: int):

@@ -1857,6 +1857,8 @@ const char* dm0_last_error(const dm0_ctx* c) {
   return c->err.c_str();
 }
 
+int dm0_device(const dm0_ctx* c) { return c ? c->device : -1; }
+
 void dm0_destroy(dm0_ctx* c) {
   if (!c) return;
   for (auto& kv : c->graphs) cudaGraphExecDestroy(kv.second.exec);

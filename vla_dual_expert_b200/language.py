@@ -11,18 +11,27 @@ and a third stream that uses one is recorded by the caller (Tensor.record_stream
 """
 from __future__ import annotations
 
-torch = _C = None   # bound by the first Engine: building and packing need neither
+
+class _Unbound:
+    """In place of the native module until an operator is called: an Engine's other calls need neither it nor torch."""
+
+    def __getattr__(self, name):
+        _bind()
+        return getattr(_C, name)
+
+
+_C = _Unbound()
 
 
 def _bind():
-    global torch, _C
-    if torch is None:
-        import torch as t      # before the native module, which links against its libraries
+    global _C
+    if isinstance(_C, _Unbound):
+        import torch  # noqa: F401  (before the native module, which links against its libraries)
         try:
             from . import _language
         except ImportError as e:
             raise ImportError(f"_language.so did not load ({e}); run `python -m vla_dual_expert_b200.build`") from e
-        torch, _C = t, _language
+        _C = _language
 
 
 def _handle(stream):
@@ -30,13 +39,7 @@ def _handle(stream):
 
 
 class LanguageOps:
-    """Mixed into Engine, whose context handle and status check it uses."""
-
-    def _bind_language(self):
-        _bind()   # before a context is made: a missing module leaves nothing behind
-
-    def _open_language(self):
-        self.device = torch.cuda.current_device()   # the context's: the tensors of these operators live there
+    """Mixed into Engine, whose context handle, device and status check it uses."""
 
     def _done(self, r):
         """The native call's outputs; a status instead of them raises."""
@@ -55,6 +58,7 @@ class LanguageOps:
     def prefill_tokens(self, image_emb, table, ids, scale: float = 1.0):
         """Prefix pass over [image rows; text rows] on the current stream: image_emb CUDA bf16 [B][Ti][hidden_v], and
         the table's rows of ids [B][Tt] behind them.  Returns the prefix it passed to prefill, [B][Ti + Tt][hidden_v]."""
+        import torch
         B, Ti, H = image_emb.shape
         if ids.dim() != 2 or ids.shape[0] != B:
             raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [{B}][Tt]")
