@@ -5,6 +5,8 @@ import subprocess
 import sys
 import types
 
+import pytest
+
 
 from vla_dual_expert_b200 import build
 
@@ -15,6 +17,8 @@ DIMS = types.SimpleNamespace(layers=1, hidden_v=128, inter_v=128, hidden_a=128, 
 # a library whose contexts are numbers, for a machine without a GPU
 FAKE = """
 import types
+
+import pytest
 import vla_dual_expert_b200 as pkg
 
 class Lib:
@@ -57,3 +61,30 @@ def test_device_of_no_context():
     build.build()
     from vla_dual_expert_b200 import load_library
     assert load_library().dm0_device(None) == -1
+
+
+def test_another_torch_or_interpreter_rebuilds_the_binding(tmp_path, monkeypatch):
+    """Without running the compiler: which builds are asked for."""
+    build.build()
+    assert build._binding_fresh()
+    calls = []
+
+    class Done(Exception):
+        pass
+
+    def run(cmd, **kw):
+        calls.append(cmd)
+        raise Done
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    assert build.build_binding() == build.BINDING and not calls
+    for change in (lambda m: m.setattr(build.importlib.metadata, "version", lambda name: "2.99.0"),
+                   lambda m: m.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399-x86_64-linux-gnu"),
+                   lambda m: m.setattr(build, "BINDING_STAMP", str(tmp_path / "missing")),
+                   lambda m: m.setattr(build, "BINDING_FLAGS", ["-O3"])):
+        with monkeypatch.context() as m:
+            change(m)
+            assert not build._binding_fresh()
+            with pytest.raises(Done):
+                build.build_binding()
+    assert len(calls) == 4 and all("binding.cpp" in " ".join(c) for c in calls)
