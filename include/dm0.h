@@ -550,6 +550,10 @@ dm0_status dm0_clear_error(dm0_ctx* ctx);
 /* Human-readable description of the last failure on `ctx` (never NULL). */
 const char* dm0_last_error(const dm0_ctx* ctx);
 
+/* What the calling thread's last call that failed with a description said, with or without a context ("" before the
+ * first; never NULL): the arguments of the language operators are checked before the context is. */
+const char* dm0_last_refusal(void);
+
 /* CUDA device that was current at dm0_create (-1 without a context). */
 int dm0_device(const dm0_ctx* ctx);
 

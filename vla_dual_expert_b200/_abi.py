@@ -26,7 +26,7 @@ EXPORTS = ("dm0_create", "dm0_weights_bytes", "dm0_load_weights", "dm0_prefill",
            "dm0_kv_commit", "dm0_denoise", "dm0_infer_host", "dm0_merged_layer", "dm0_op_gemm",
            "dm0_op_attention", "dm0_attention_noalloc", "dm0_debug_view", "dm0_launch_count", "dm0_probe",
            "dm0_probe_read", "dm0_selftest_timeout", "dm0_sync", "dm0_device_error", "dm0_clear_error", "dm0_last_error",
-           "dm0_device", "dm0_destroy", "dm0_pack_e4m3_rows", "dm0_set_prefix_fp8", "dm0_op_quant_e4m3",
+           "dm0_device", "dm0_last_refusal", "dm0_destroy", "dm0_pack_e4m3_rows", "dm0_set_prefix_fp8", "dm0_op_quant_e4m3",
            "dm0_op_gemm_e4m3", "dm0_grad_floats", "dm0_train_step", "dm0_prepare", "dm0_embed", "dm0_embed_grad",
            "dm0_embed_grad_workspace", "dm0_residual_norm", "dm0_residual_norm_grad",
            "dm0_residual_norm_grad_workspace", "dm0_vocab_loss", "dm0_vocab_loss_workspace", "dm0_vocab_loss_grad",
@@ -85,6 +85,7 @@ def load_library() -> ctypes.CDLL:
         "dm0_debug_view": (c_int, [P, ctypes.c_char_p, ctypes.POINTER(P)]),
         "dm0_launch_count": (ctypes.c_uint64, [P]),
         "dm0_device": (c_int, [P]),
+        "dm0_last_refusal": (ctypes.c_char_p, []),
         "dm0_probe": (c_int, [P, c_int]),
         "dm0_probe_read": (c_int, [P, c_int, ctypes.POINTER(c_int), ctypes.POINTER(ctypes.c_double)]),
         "dm0_selftest_timeout": (c_int, [P, c_int, P]),

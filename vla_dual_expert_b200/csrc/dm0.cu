@@ -207,7 +207,10 @@ struct dm0_ctx {
 
 namespace {
 
+thread_local std::string last_refusal;
+
 dm0_status fail(dm0_ctx* c, dm0_status st, const std::string& msg) {
+  last_refusal = msg;
   if (c) c->err = msg;
   return st;
 }
@@ -1856,6 +1859,8 @@ const char* dm0_last_error(const dm0_ctx* c) {
   if (!c) return "null context";
   return c->err.c_str();
 }
+
+const char* dm0_last_refusal(void) { return last_refusal.c_str(); }
 
 int dm0_device(const dm0_ctx* c) { return c ? c->device : -1; }
 

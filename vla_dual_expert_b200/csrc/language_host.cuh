@@ -13,7 +13,7 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 // The context part of every entry's checks: its device must be the current one.
 dm0_status lang_enter(dm0_ctx* c) {
-  if (!c) return DM0_EINVAL;
+  if (!c) return fail(c, DM0_EINVAL, "null context");
   int dev = -1;
   CK(cudaGetDevice(&dev));
   if (dev != c->device)
