@@ -167,3 +167,18 @@ def test_a_refusal_is_the_calling_threads(abi):  # noqa: F811
     t.join()
     assert said == [b""] and lib.dm0_last_refusal().decode() == SIZES
     assert lib.dm0_last_error(None) == b"null context"
+
+
+@pytest.mark.parametrize("bad", [dict(B=0), dict(T=0), dict(vocab=0), dict(vocab=(1 << 22) + 1), dict(hidden=4),
+                                 dict(hidden=12), dict(hidden=65544)])
+def test_no_workspace_for_refused_table_gradients(abi, bad):  # noqa: F811
+    a = {**dict(B=2, T=3, vocab=10, hidden=64), **bad}
+    assert abi.load_library().dm0_embed_grad_workspace(*a.values()) == 0
+
+
+@pytest.mark.parametrize("bad", [dict(tokens=0), dict(tokens=(1 << 24) + 1), dict(vocab=0), dict(vocab=(1 << 22) + 1),
+                                 dict(hidden=32), dict(hidden=96), dict(hidden=65600)])
+def test_no_workspace_for_refused_losses(abi, bad):  # noqa: F811
+    a = {**dict(tokens=5, vocab=100, hidden=128), **bad}
+    lib = abi.load_library()
+    assert lib.dm0_vocab_loss_workspace(*a.values()) == 0 and lib.dm0_vocab_loss_grad_workspace(*a.values()) == 0

@@ -28,6 +28,14 @@ bool lang_tokens_ok(int B, int T) {
 }
 
 // ---------------------------------------------------------------- embedding
+// (every call's size checks, which its workspace function shares)
+dm0_status embed_sizes_ok(dm0_ctx* c, int B, int T, int vocab, int hidden) {
+  if (!lang_tokens_ok(B, T) || vocab < 1 || vocab > kLangMaxVocab) return fail(c, DM0_ESHAPE, "bad batch, tokens or vocab");
+  if (hidden < 8 || hidden % 8 != 0 || hidden > kLangMaxHidden)
+    return fail(c, DM0_ESHAPE, "hidden must be a multiple of 8, at most 65536");
+  return DM0_OK;
+}
+
 dm0_status rows_ok(dm0_ctx* c, const void* p, int f32, int T, int H, int64_t batch, int64_t row) {
   const int vec = f32 ? 4 : 8;
   if (row < H || batch < 0 || row % vec != 0 || batch % vec != 0 || !aligned16(p))
@@ -275,11 +283,15 @@ VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
   return p;
 }
 
-dm0_status vocab_ok(dm0_ctx* c, const void* h, const void* w, const void* t, int tokens, int vocab, int H) {
-  if (!h || !w || !t) return fail(c, DM0_EINVAL, "null argument");
+dm0_status vocab_sizes_ok(dm0_ctx* c, int tokens, int vocab, int H) {
   if (tokens < 1 || tokens > kLangMaxTokens || vocab < 1 || vocab > kLangMaxVocab)
     return fail(c, DM0_ESHAPE, "tokens or vocab out of range");
   if (H < 64 || H % 64 != 0 || H > kLangMaxHidden) return fail(c, DM0_ESHAPE, "hidden must be a multiple of 64");
+  return DM0_OK;
+}
+dm0_status vocab_ok(dm0_ctx* c, const void* h, const void* w, const void* t, int tokens, int vocab, int H) {
+  if (!h || !w || !t) return fail(c, DM0_EINVAL, "null argument");
+  TRY(vocab_sizes_ok(c, tokens, vocab, H));
   if (!aligned16(h) || !aligned16(w)) return fail(c, DM0_EINVAL, "hidden states and weights must be 16-byte aligned");
   return DM0_OK;
 }
@@ -462,9 +474,7 @@ extern "C" {
 dm0_status dm0_embed(dm0_ctx* c, const void* table, const void* ids, int ids_i64, int B, int T, int vocab, int hidden,
                      float scale, void* out, int out_f32, int64_t batch_stride, int64_t row_stride, void* stream) {
   if (!table || !ids || !out) return fail(c, DM0_EINVAL, "null argument");
-  if (!lang_tokens_ok(B, T) || vocab < 1 || vocab > kLangMaxVocab) return fail(c, DM0_ESHAPE, "bad batch, tokens or vocab");
-  if (hidden < 8 || hidden % 8 != 0 || hidden > kLangMaxHidden)
-    return fail(c, DM0_ESHAPE, "hidden must be a multiple of 8, at most 65536");
+  TRY(embed_sizes_ok(c, B, T, vocab, hidden));
   if (!aligned16(table)) return fail(c, DM0_EINVAL, "the table must be 16-byte aligned");
   TRY(rows_ok(c, out, out_f32, T, hidden, batch_stride, row_stride));
   if (B > 1 && batch_stride < (T - 1) * row_stride + hidden && (batch_stride < hidden || row_stride < (B - 1) * batch_stride + hidden))
@@ -480,7 +490,7 @@ dm0_status dm0_embed(dm0_ctx* c, const void* table, const void* ids, int ids_i64
 }
 
 size_t dm0_embed_grad_workspace(int B, int T, int vocab, int hidden) {
-  if (!lang_tokens_ok(B, T) || vocab < 1 || vocab > kLangMaxVocab || hidden < 8 || hidden > kLangMaxHidden) return 0;
+  if (embed_sizes_ok(nullptr, B, T, vocab, hidden) != DM0_OK) return 0;
   return emb_grad_plan(B * T, vocab, hidden).bytes;
 }
 
@@ -488,9 +498,7 @@ dm0_status dm0_embed_grad(dm0_ctx* c, const void* ids, int ids_i64, int B, int T
                           const void* dout, int dout_f32, int64_t batch_stride, int64_t row_stride, float* grad,
                           int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
   if (!ids || !dout || !grad || !workspace) return fail(c, DM0_EINVAL, "null argument");
-  if (!lang_tokens_ok(B, T) || vocab < 1 || vocab > kLangMaxVocab) return fail(c, DM0_ESHAPE, "bad batch, tokens or vocab");
-  if (hidden < 8 || hidden % 8 != 0 || hidden > kLangMaxHidden)
-    return fail(c, DM0_ESHAPE, "hidden must be a multiple of 8, at most 65536");
+  TRY(embed_sizes_ok(c, B, T, vocab, hidden));
   if (!aligned16(grad) || !aligned16(workspace)) return fail(c, DM0_EINVAL, "grad and workspace must be 16-byte aligned");
   TRY(rows_ok(c, dout, dout_f32, T, hidden, batch_stride, row_stride));
   if (workspace_bytes < emb_grad_plan(B * T, vocab, hidden).bytes) return fail(c, DM0_EINVAL, "workspace too small");
@@ -574,7 +582,7 @@ dm0_status dm0_residual_norm_grad(dm0_ctx* c, const dm0_norm* a, const void* dn,
 }
 
 size_t dm0_vocab_loss_workspace(int tokens, int vocab, int hidden) {
-  if (tokens < 1 || tokens > kLangMaxTokens || vocab < 1 || vocab > kLangMaxVocab || hidden < 64) return 0;
+  if (vocab_sizes_ok(nullptr, tokens, vocab, hidden) != DM0_OK) return 0;
   return vocab_loss_plan(tokens, vocab).bytes;
 }
 
@@ -592,9 +600,7 @@ dm0_status dm0_vocab_loss(dm0_ctx* c, const void* hidden_states, const void* wei
 }
 
 size_t dm0_vocab_loss_grad_workspace(int tokens, int vocab, int hidden) {
-  if (tokens < 1 || tokens > kLangMaxTokens || vocab < 1 || vocab > kLangMaxVocab || hidden < 64 ||
-      hidden > kLangMaxHidden)
-    return 0;
+  if (vocab_sizes_ok(nullptr, tokens, vocab, hidden) != DM0_OK) return 0;
   return vocab_grad_plan(tokens, vocab, hidden).bytes;
 }
 
