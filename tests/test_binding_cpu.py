@@ -57,6 +57,17 @@ def test_a_native_module_that_does_not_load_is_named_by_the_first_operator():
     assert len(lines) == 2 and all("_language.so" in x and "vla_dual_expert_b200.build" in x for x in lines)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+def test_prefill_tokens_takes_no_other_image_rows(dtype):
+    """Image rows of another type are refused and not rounded in passing, host tensors as everywhere."""
+    import torch
+    build.build()
+    from vla_dual_expert_b200.language import LanguageOps
+    ids = torch.zeros(2, 3, dtype=torch.int64)
+    with pytest.raises(TypeError, match="image_emb must be a CUDA torch.bfloat16 tensor"):
+        LanguageOps().prefill_tokens(torch.zeros(2, 4, 64, dtype=getattr(torch, dtype)), None, ids)
+
+
 def test_device_of_no_context():
     build.build()
     from vla_dual_expert_b200 import load_library

@@ -57,11 +57,15 @@ class LanguageOps:
 
     def prefill_tokens(self, image_emb, table, ids, scale: float = 1.0):
         """Prefix pass over [image rows; text rows] on the current stream: image_emb CUDA bf16 [B][Ti][hidden_v], and
-        the table's rows of ids [B][Tt] behind them.  Returns the prefix it passed to prefill, [B][Ti + Tt][hidden_v]."""
+        the table's rows of ids [B][Tt] behind them.  Returns the prefix it passed to prefill, [B][Ti + Tt][hidden_v].
+        The image rows are copied there; a program that makes them in its own prefix tensor has no copy with
+        embed(table, ids, out=prefix[:, Ti:]) and prefill(prefix)."""
         import torch
         B, Ti, H = image_emb.shape
         if ids.dim() != 2 or ids.shape[0] != B:
             raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [{B}][Tt]")
+        if not image_emb.is_cuda or image_emb.dtype != torch.bfloat16:
+            raise TypeError("image_emb must be a CUDA torch.bfloat16 tensor")
         prefix = torch.empty(B, Ti + ids.shape[1], H, dtype=torch.bfloat16, device=image_emb.device)
         prefix[:, :Ti] = image_emb
         self.embed(table, ids, scale, out=prefix[:, Ti:])
