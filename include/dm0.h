@@ -480,6 +480,7 @@ size_t dm0_vocab_loss_workspace(int tokens, int vocab, int hidden);
  * Of a target, 1 - softmax keeps its own bits (lse is of the same logits, rounded to fp32: 2^-24 of lse in 1 - softmax).
  * The products are added by the tensor cores in fp32, toward zero, in stretches of at most 16384 entries or tokens, and
  * the stretches rounded to nearest: sums of one sign are up to 1e-4 of themselves too small.
+ * A token without a target adds its hidden state times zero to dweight: such states have to be finite.
  * The logits are built again, in pieces of the vocabulary of at most 2^27 entries (256 MB of the workspace) or 256
  * columns. */
 dm0_status dm0_vocab_loss_grad(dm0_ctx* ctx, const void* hidden_states, const void* weight, const void* targets,

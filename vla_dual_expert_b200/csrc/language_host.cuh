@@ -97,7 +97,6 @@ dm0_status embed_grad_run(dm0_ctx* c, cudaStream_t s, dm0::Ids ids, int n, const
   const int zero_ctas = (zero_rows + dm0::kEmbZeroRows - 1) / dm0::kEmbZeroRows;
   TRY(launch(c, s, dm0::embed_sum_kernel<Td>, dim3(p.tiles * p.slices + zero_ctas), dim3(256), 0, o, dout, v, H, scale,
              grad, accumulate, p.tiles, p.slices, zero_rows));
-  if (p.tiles < 2) return DM0_OK;   // no segment is longer than a tile
   return launch(c, s, dm0::embed_join_kernel,
                 dim3((p.tiles + dm0::kFixTiles - 1) / dm0::kFixTiles, (H + dm0::kFixCols - 1) / dm0::kFixCols),
                 dim3(256), 0, o, p.tiles, H, scale, grad, accumulate);
@@ -255,7 +254,8 @@ VocabGradPlan vocab_grad_plan(int tokens, int vocab, int H) {
   const int pieces = (vr + most - 1) / most;
   p.piece = ((vr + pieces - 1) / pieces + 255) / 256 * 256;
   // splits of dh's contraction over the piece: the time of the busiest worker, whose tiles of dh and dW come in
-  // turn (0.28 us a k-block, 1 us a tile), against the traffic of the fp32 sums
+  // turn (0.28 us a k-block, 1 us a tile: of a pair's 256 x 256; the 128 x 128 of up to 128 tokens, which HBM bounds, go
+  // by the same), against the traffic of the fp32 sums
   const int tile = vocab_tile(tokens), workers = vocab_pairs(tokens) ? kLangSms / 2 : kLangSms;
   const int cols = std::min(p.piece, vocab);
   const int64_t ht = (H + tile - 1) / tile, th = (tokens + tile - 1) / tile * ht, tw = (cols + tile - 1) / tile * ht;

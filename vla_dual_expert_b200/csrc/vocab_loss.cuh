@@ -24,8 +24,10 @@
 // tokens x 131072 x 2048 takes 1.67 ms one after another, 1320 TFLOP/s (the library's bf16 product that writes those
 // logits 1.74 ms), the gradients of 8192 tokens 10.5 ms, 1260 TFLOP/s (the library's three products 10.0 ms).  With
 // few tokens they are bound by HBM: the loss reads W once (7 tokens: 91 us alone, 103 among calls with other
-// weights, 82 at the rate of a copy); the gradient twice, as its second product needs G's whole rows, and dW is
-// written (316 us, 245 at that rate).
+// weights, 82 at the rate of a copy); the gradient twice, once for the logits and once for dh, in launches of their own,
+// and dW is written (7 tokens: 294 to 318 us between one B200 and another, 245 at that rate; with one reading it would
+// be 164, as lse is given and a tile's G is known with its logits).  dW in fp32 passes through shared memory and plain
+// stores: 412 us, 986 where it is added to what is there (327 and 491 at that rate).
 #pragma once
 #include "attention_tc.cuh"   // sw128_mnmajor_desc, tmem_st32
 #include "embedding.cuh"

@@ -114,6 +114,7 @@ class LanguageOps:
         """Gradients of sum(dloss * loss) of vocab_loss with respect to hidden and weight (dm0_vocab_loss_grad).
 
         lse, dloss: f32 [tokens].  dhidden [tokens][H] and dweight [vocab][H] are bf16 unless an fp32 tensor is
-        given; False leaves that gradient out.  accumulate adds to an fp32 dweight.  Returns (dhidden, dweight)."""
+        given; False leaves that gradient out.  accumulate adds to an fp32 dweight.  The hidden states of tokens without
+        a target have to be finite (dweight takes them times zero).  Returns (dhidden, dweight)."""
         return self._done(_C.vocab_loss_grad(self.h.value or 0, self.device, hidden, weight, targets, lse, dloss,
                                              dhidden, dweight, accumulate, _handle(stream)))
