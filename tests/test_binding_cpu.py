@@ -68,6 +68,17 @@ def test_prefill_tokens_takes_no_other_image_rows(dtype):
         LanguageOps().prefill_tokens(torch.zeros(2, 4, 64, dtype=getattr(torch, dtype)), None, ids)
 
 
+def test_without_torch_the_library_alone_is_built(monkeypatch):
+    build.build()
+    asked = []
+    monkeypatch.setattr(build, "build_library", lambda *a: asked.append("library"))
+    monkeypatch.setattr(build, "build_binding", lambda *a: asked.append("binding"))
+    build.build()
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    assert build.build() == build.LIB
+    assert asked == ["library", "binding", "library"]
+
+
 def test_device_of_no_context():
     build.build()
     from vla_dual_expert_b200 import load_library

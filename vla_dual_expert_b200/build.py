@@ -89,7 +89,8 @@ def build_binding(force: bool = False) -> str:
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     build_library(force, ptxas_verbose)
-    build_binding(force)
+    if importlib.util.find_spec("torch"):   # the language operators take its tensors; all else runs without it
+        build_binding(force)
     return LIB
 
 
